@@ -7,6 +7,10 @@ tensors' device).  The functions carry the C ABI's names:
   dspark_markov_sample  Markov draft sampler + confidence head
   dspark_verify         exact greedy / sampled verify
   dspark_accept_stats   training-side analytic acceptance statistics
+  dspark_top_logits     a row's highest logits and the mass of the others
+  dspark_distill        distillation from a teacher's highest logits
+  dspark_beam_select    one step of a beam search; dspark_beam_reorder moves the
+                        beams' states
 
 Outputs are allocated with torch on the inputs' device (or passed in through
 `out=`).  A status other than DSPARK_OK raises DSparkError.  There is no CPU
@@ -30,16 +34,20 @@ DSPARK_OK, DSPARK_EINVAL, DSPARK_EDTYPE, DSPARK_ESHAPE, DSPARK_EWORKSPACE, DSPAR
 DSPARK_BF16, DSPARK_F32 = 1, 2
 DSPARK_OP_MARKOV, DSPARK_OP_VERIFY, DSPARK_OP_STATS, DSPARK_OP_STATS_BACKWARD = 1, 2, 3, 4
 DSPARK_OP_STATS_MARKOV = 5
+DSPARK_OP_TOP, DSPARK_OP_DISTILL, DSPARK_OP_BEAM = 6, 7, 8
 DSPARK_NOALLOC_SCRATCH_BYTES = 32 << 20  # per-GPU scratch of dspark_verify_noalloc
 DSPARK_MAX_GAMMA, DSPARK_MAX_RANK, DSPARK_MAX_VERIFY_BATCH = 16, 256, 65535  # as include/dspark.h
+DSPARK_MAX_TOP, DSPARK_MAX_TOP_VOCAB, DSPARK_MAX_BEAMS = 128, 2097152, 32
 FLAG_NEAR, FLAG_NONFINITE, FLAG_RESIDUAL_ZERO, FLAG_EMPTY_ROW, FLAG_BAD_POLICY = 1, 2, 4, 8, 16
 
 __all__ = ["DSparkError", "Policy", "lib", "dspark_markov_sample", "dspark_verify",
            "dspark_verify_noalloc",
            "dspark_accept_stats", "dspark_accept_stats_backward", "dspark_accept_stats_markov",
-           "dspark_select_width", "dspark_workspace_size", "profile_enable",
+           "dspark_select_width", "dspark_top_logits", "dspark_distill", "dspark_distill_backward",
+           "dspark_beam_select", "dspark_beam_reorder",
+           "dspark_workspace_size", "profile_enable",
            "profile_summary", "DSPARK_MAX_GAMMA", "DSPARK_MAX_RANK",
-           "DSPARK_MAX_VERIFY_BATCH"]
+           "DSPARK_MAX_VERIFY_BATCH", "DSPARK_MAX_TOP", "DSPARK_MAX_TOP_VOCAB", "DSPARK_MAX_BEAMS"]
 
 
 class DSparkError(RuntimeError):
@@ -87,6 +95,18 @@ def lib():
         L.dspark_accept_stats_backward.restype = C.c_int
         L.dspark_select_width.argtypes = [P, P, i32, i32, P, P, P]
         L.dspark_select_width.restype = C.c_int
+        L.dspark_top_logits.argtypes = [P, C.c_int, i32, i32, i32, f32, P, P, P, P, P, P, sz, P]
+        L.dspark_top_logits.restype = C.c_int
+        L.dspark_distill.argtypes = [P, C.c_int, P, P, P, P, i32, i32, i32, i32, f32, f32, P, P, P, P, P,
+                                     P, sz, P]
+        L.dspark_distill.restype = C.c_int
+        L.dspark_distill_backward.argtypes = [P, C.c_int, P, P, P, P, P, i32, i32, i32, i32, f32, f32, P,
+                                              P, P]
+        L.dspark_distill_backward.restype = C.c_int
+        L.dspark_beam_select.argtypes = [P, C.c_int, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, sz, P]
+        L.dspark_beam_select.restype = C.c_int
+        L.dspark_beam_reorder.argtypes = [P, P, P, P, C.c_int64, i32, i32, i32, i32, i32, C.c_int64, P]
+        L.dspark_beam_reorder.restype = C.c_int
         L.dspark_profile_enable.argtypes = [C.c_int]
         L.dspark_profile_enable.restype = C.c_int
         L.dspark_markov_plan.argtypes = [C.c_int]
@@ -443,6 +463,207 @@ def dspark_select_width(confidence, cost, want_expected=True, out=None):
             _dev_tensor(out["expected"], torch.float32, "out['expected']", (B,), dev)
     rc = lib().dspark_select_width(_p(confidence), _p(cost), B, g, _p(out["n_draft"]),
                                    _p(out["expected"]), _stream(dev))
+    _check(rc)
+    return out
+
+
+def _scratch(op, device, nbytes):
+    """Workspace of one call.  Outside a stream capture it is the cached one of
+    (device, stream, op).  A captured call gets memory of its graph's own pool:
+    a graph keeps using the address, so a buffer that eager calls share and may
+    replace by a larger one would not do, nor one that two graphs share."""
+    if nbytes == 0:
+        return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    ws = _workspace(op, device, nbytes)
+    return ws, ws.numel()
+
+
+def _outputs(what, spec, out, device):
+    """The output tensors of (name, dtype, shape): allocated, or the caller's, checked."""
+    if out is None:
+        return {name: torch.empty(shape, dtype=dtype, device=device) for name, dtype, shape in spec}
+    _check_out(out, spec, device, what)
+    return out
+
+
+def dspark_top_logits(logits, k, temperature=1.0, out=None):
+    """The k highest logits of each row of logits [..., V] (bfloat16 or
+    float32) and the mass of the others; returns a dict of device tensors
+    top_values [..., k] f32 (descending, -inf: none), top_ids [..., k] int32
+    (-1: none), rest and lse [...] f32 (log-sum-exp of logits / temperature
+    over the tokens not listed and over all), flags [...] uint8."""
+    dt = _logits_dtype(logits, "logits")
+    _dev_tensor(logits, logits.dtype, "logits")
+    if logits.dim() < 1:
+        raise DSparkError("top_logits: logits must be [..., V]")
+    *lead, V = logits.shape
+    k = int(k)
+    if k < 0:
+        raise DSparkError("top_logits: k must be positive")
+    R = 1
+    for n in lead:
+        R *= n
+    if R > 0x7fffffff or V > 0x7fffffff:
+        raise DSparkError("top_logits: logits have too many rows or tokens")
+    dev = logits.device
+    with torch.cuda.device(dev):
+        out = _outputs("top_logits", [("top_values", torch.float32, (*lead, k)),
+                                      ("top_ids", torch.int32, (*lead, k)), ("rest", torch.float32, lead),
+                                      ("lse", torch.float32, lead), ("flags", torch.uint8, lead)], out, dev)
+        ws, nb = _scratch(DSPARK_OP_TOP, dev, dspark_workspace_size(DSPARK_OP_TOP, R, 1, V, k))
+        rc = lib().dspark_top_logits(_p(logits), dt, R, V, k, float(temperature), _p(out["top_values"]),
+                                     _p(out["top_ids"]), _p(out["rest"]), _p(out["lse"]),
+                                     _p(out["flags"]), _p(ws), nb, _stream(dev))
+    _check(rc)
+    return out
+
+
+def _distill_args(what, draft, values, ids, teacher_rest, block_mask):
+    """Checks shared by the distillation calls; returns (dtype, N, gamma, V, K)."""
+    dt = _logits_dtype(draft, "draft")
+    _dev_tensor(draft, draft.dtype, "draft")
+    if draft.dim() != 3:
+        raise DSparkError(f"{what}: draft must be [N, gamma, V]")
+    N, g, V = draft.shape
+    dev = draft.device
+    _dev_tensor(values, torch.float32, "teacher_values", device=dev)
+    if values.dim() != 3:
+        raise DSparkError(f"{what}: teacher_values must be [N, gamma, K]")
+    K = values.shape[2]
+    _dev_tensor(values, torch.float32, "teacher_values", (N, g, K))
+    _dev_tensor(ids, torch.int32, "teacher_ids", (N, g, K), dev)
+    if teacher_rest is not None:
+        _dev_tensor(teacher_rest, torch.float32, "teacher_rest", (N, g), dev)
+    if block_mask is not None:
+        _dev_tensor(block_mask, torch.uint8, "block_mask", (N,), dev)
+    return dt, N, g, V, K
+
+
+def dspark_distill(draft, teacher_values, teacher_ids, teacher_rest=None, block_mask=None,
+                   temperature=1.0, weight=1.0, out=None):
+    """Distillation loss of draft logits [N, gamma, V] towards a teacher's
+    highest logits (dspark_top_logits' top_values, top_ids and, for its
+    remaining mass as one more outcome, rest); returns a dict of device tensors
+    kl, lse, rest [N, gamma] f32, flags [N, gamma] uint8 and sums [4] f32."""
+    dt, N, g, V, K = _distill_args("distill", draft, teacher_values, teacher_ids, teacher_rest, block_mask)
+    dev = draft.device
+    with torch.cuda.device(dev):
+        out = _outputs("distill", [("kl", torch.float32, (N, g)), ("lse", torch.float32, (N, g)),
+                                   ("rest", torch.float32, (N, g)), ("flags", torch.uint8, (N, g)),
+                                   ("sums", torch.float32, (4,))], out, dev)
+        ws, nb = _scratch(DSPARK_OP_DISTILL, dev, dspark_workspace_size(DSPARK_OP_DISTILL, N, g, V))
+        rc = lib().dspark_distill(_p(draft), dt, _p(teacher_values), _p(teacher_ids), _p(teacher_rest),
+                                  _p(block_mask), N, g, V, K, float(temperature), float(weight),
+                                  _p(out["kl"]), _p(out["lse"]), _p(out["rest"]), _p(out["flags"]),
+                                  _p(out["sums"]), _p(ws), nb, _stream(dev))
+    _check(rc)
+    return out
+
+
+def dspark_distill_backward(draft, teacher_values, teacher_ids, rest, teacher_rest=None,
+                            block_mask=None, temperature=1.0, weight=1.0, grad_scale=None, out=None):
+    """Gradient of grad_scale x dspark_distill's sums[0] into the draft logits;
+    rest is the one dspark_distill returned for the same inputs.  Returns a dict
+    with grad_draft [N, gamma, V] (the logits dtype).  grad_scale: a one-element
+    float32 device tensor or None (1)."""
+    dt, N, g, V, K = _distill_args("distill_backward", draft, teacher_values, teacher_ids, teacher_rest,
+                                   block_mask)
+    dev = draft.device
+    _dev_tensor(rest, torch.float32, "rest", (N, g), dev)
+    if grad_scale is not None:
+        _dev_tensor(grad_scale, torch.float32, "grad_scale", device=dev)
+        if grad_scale.numel() != 1:
+            raise DSparkError("distill_backward: grad_scale must hold one value")
+    with torch.cuda.device(dev):
+        out = _outputs("distill_backward", [("grad_draft", draft.dtype, (N, g, V))], out, dev)
+        rc = lib().dspark_distill_backward(_p(draft), dt, _p(teacher_values), _p(teacher_ids), _p(rest),
+                                           _p(teacher_rest), _p(block_mask), N, g, V, K,
+                                           float(temperature), float(weight), _p(grad_scale),
+                                           _p(out["grad_draft"]), _stream(dev))
+    _check(rc)
+    return out
+
+
+def dspark_beam_select(logits, scores, picks, finished=None, eos_token=0, out=None):
+    """One beam-search step over logits [B, W, V] and the beams' scores [B, W]
+    f32: the `picks` best continuations of each request; returns a dict of device
+    tensors tokens, parents [B, picks] int32 (-1: none), scores [B, picks] f32
+    and flags [B, W] uint8.  finished [B, W] uint8: beams that go on as one
+    candidate (eos_token, their score)."""
+    dt = _logits_dtype(logits, "logits")
+    _dev_tensor(logits, logits.dtype, "logits")
+    if logits.dim() != 3:
+        raise DSparkError("beam_select: logits must be [B, W, V]")
+    B, W, V = logits.shape
+    M = int(picks)
+    if M < 0:
+        raise DSparkError("beam_select: picks must be positive")
+    dev = logits.device
+    _dev_tensor(scores, torch.float32, "scores", (B, W), dev)
+    if finished is not None:
+        _dev_tensor(finished, torch.uint8, "finished", (B, W), dev)
+    with torch.cuda.device(dev):
+        out = _outputs("beam_select", [("tokens", torch.int32, (B, M)), ("parents", torch.int32, (B, M)),
+                                       ("scores", torch.float32, (B, M)), ("flags", torch.uint8, (B, W))],
+                       out, dev)
+        ws, nb = _scratch(DSPARK_OP_BEAM, dev, dspark_workspace_size(DSPARK_OP_BEAM, B, W, V, M))
+        rc = lib().dspark_beam_select(_p(logits), dt, _p(scores), _p(finished), int(eos_token), B, W, V, M,
+                                      _p(out["tokens"]), _p(out["parents"]), _p(out["scores"]),
+                                      _p(out["flags"]), _p(ws), nb, _stream(dev))
+    _check(rc)
+    return out
+
+
+def dspark_beam_reorder(state, parents, batch_dim=0, lengths=None, length_dim=None, out=None):
+    """The beams' states in the order of a selection: out[..., b, j, ...] =
+    state[..., b, parents[b, j], ...], where dimensions batch_dim and batch_dim
+    + 1 of state are the requests and their beams and parents is [B, M] int32.
+    With lengths [B] int32 only positions before lengths[b] of dimension
+    length_dim are moved.  Positions that are not moved, and rows whose parent is
+    -1, keep what out holds (zeros where out is allocated here).  out=state
+    reorders in place.  Returns out."""
+    if not isinstance(state, torch.Tensor):
+        raise DSparkError("beam_reorder: state must be a GPU tensor")
+    _dev_tensor(state, state.dtype, "state")
+    dev = state.device
+    d = int(batch_dim)
+    if d < 0 or d + 1 >= state.dim():
+        raise DSparkError("beam_reorder: batch_dim must name two dimensions of state")
+    _dev_tensor(parents, torch.int32, "parents", device=dev)
+    B, W = state.shape[d], state.shape[d + 1]
+    if parents.dim() != 2 or parents.shape[0] != B:
+        raise DSparkError("beam_reorder: parents must be [B, M]")
+    M = parents.shape[1]
+    if (lengths is None) != (length_dim is None):
+        raise DSparkError("beam_reorder: lengths and length_dim go together")
+    outer = inner = S = T = 1
+    for n in state.shape[:d]:
+        outer *= n
+    if lengths is None:
+        for n in state.shape[d + 2:]:
+            inner *= n
+    else:
+        _dev_tensor(lengths, torch.int32, "lengths", (B,), dev)
+        t = int(length_dim)
+        if t < d + 2 or t >= state.dim():
+            raise DSparkError("beam_reorder: length_dim must be a dimension after the beams")
+        T = state.shape[t]
+        for n in state.shape[d + 2:t]:
+            S *= n
+        for n in state.shape[t + 1:]:
+            inner *= n
+    shape = (*state.shape[:d + 1], M, *state.shape[d + 2:])
+    if max(B, W, M, S, T) > 0x7fffffff:
+        raise DSparkError("beam_reorder: a dimension is too large")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.zeros(shape, dtype=state.dtype, device=dev)
+        else:
+            _dev_tensor(out, state.dtype, "out", shape, dev)
+        rc = lib().dspark_beam_reorder(_p(state), _p(out), _p(parents), _p(lengths), outer, B, W, M, S, T,
+                                       inner * state.element_size(), _stream(dev))
     _check(rc)
     return out
 

@@ -3,6 +3,7 @@
 // per-operation launchers.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "dspark.h"
@@ -68,6 +69,29 @@ dspark_status verify_args(const void* target_logits, int logits_dtype, const int
   return DSPARK_OK;
 }
 
+// Logits pointer aligned to its element type.
+bool aligned_to(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == DSPARK_BF16 ? 1u : 3u)) == 0;
+}
+
+bool temperature_ok(float t) { return t >= 0x1p-20f && t <= 0x1p20f; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+size_t logit_bytes(int dtype) { return dtype == DSPARK_BF16 ? 2 : 4; }
+
+// Checks shared by dspark_distill and its backward (everything but pointers).
+dspark_status distill_sizes(int dtype, int32_t N, int32_t gamma, int32_t V, int32_t K, float temperature) {
+  if (N < 0 || K <= 0) return DSPARK_EINVAL;
+  const dspark_status s = check_common(dtype, gamma, V);
+  if (s != DSPARK_OK) return s;
+  if (K > DSPARK_MAX_TOP || static_cast<int64_t>(N) * gamma > 0x7fffffffLL) return DSPARK_ESHAPE;
+  return temperature_ok(temperature) ? DSPARK_OK : DSPARK_EINVAL;
+}
+
 size_t verify_bytes(int dtype, int32_t B, int32_t gamma, int32_t V) {
   const size_t a = dspark::plan_verify(dtype, B, gamma, V, true).bytes;
   const size_t b = dspark::plan_verify(dtype, B, gamma, V, false).bytes;
@@ -94,6 +118,15 @@ size_t dspark_workspace_size(int op, int32_t B, int32_t gamma, int32_t V, int32_
       return dspark::plan_stats_backward(B, gamma, V).bytes;
     case DSPARK_OP_STATS_MARKOV:
       return dspark::plan_stats_markov(B, gamma, V).bytes;
+    case DSPARK_OP_TOP:
+      return r <= 0 || r > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB ? 0 : dspark::plan_top(B, V, r).bytes;
+    case DSPARK_OP_DISTILL:
+      return dspark::plan_distill(B, gamma, V).bytes;
+    case DSPARK_OP_BEAM:
+      return r <= 0 || r > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB || gamma > DSPARK_MAX_BEAMS ||
+                     static_cast<int64_t>(B) * gamma > 0x7fffffffLL
+                 ? 0
+                 : dspark::plan_beam(B, gamma, V, r).bytes;
     default:
       return 0;
   }
@@ -269,6 +302,103 @@ dspark_status dspark_select_width(const float* confidence, const float* cost, in
   if (B == 0) return DSPARK_OK;
   if (!confidence || !n_draft) return DSPARK_EINVAL;
   const hipError_t e = dspark::launch_select_width(confidence, cost, B, gamma, n_draft, expected,
+                                                   static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
+}
+
+dspark_status dspark_top_logits(const void* logits, int logits_dtype, int32_t R, int32_t V, int32_t K,
+                                float temperature, float* top_values, int32_t* top_ids, float* rest, float* lse,
+                                uint8_t* flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (R < 0 || V <= 0 || K <= 0) return DSPARK_EINVAL;
+  if (logits_dtype != DSPARK_BF16 && logits_dtype != DSPARK_F32) return DSPARK_EDTYPE;
+  if (K > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB) return DSPARK_ESHAPE;
+  if (!temperature_ok(temperature)) return DSPARK_EINVAL;
+  if (R == 0) return DSPARK_OK;
+  if (!logits || !top_values || !top_ids || !rest || !lse || !flags || !aligned_to(logits, logits_dtype))
+    return DSPARK_EINVAL;
+  const dspark::TopPlan plan = dspark::plan_top(R, V, K);
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return DSPARK_EWORKSPACE;
+  const hipError_t e = dspark::launch_top(logits, logits_dtype, R, V, K, temperature, top_values, top_ids, rest, lse,
+                                          flags, workspace, plan, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
+}
+
+dspark_status dspark_distill(const void* draft_logits, int logits_dtype, const float* teacher_values,
+                             const int32_t* teacher_ids, const float* teacher_rest, const uint8_t* block_mask,
+                             int32_t N, int32_t gamma, int32_t V, int32_t K, float temperature, float weight,
+                             float* kl, float* lse, float* rest, uint8_t* flags, float* sums, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const dspark_status s = distill_sizes(logits_dtype, N, gamma, V, K, temperature);
+  if (s != DSPARK_OK) return s;
+  if (!sums) return DSPARK_EINVAL;
+  if (N > 0 && (!draft_logits || !teacher_values || !teacher_ids || !kl || !lse || !rest || !flags ||
+                !aligned_to(draft_logits, logits_dtype)))
+    return DSPARK_EINVAL;
+  const dspark::DistillPlan plan = dspark::plan_distill(N, gamma, V);
+  if (N > 0 && (!workspace || workspace_bytes < plan.bytes)) return DSPARK_EWORKSPACE;
+  const hipError_t e = dspark::launch_distill(draft_logits, logits_dtype, teacher_values, teacher_ids, teacher_rest,
+                                              block_mask, N, gamma, V, K, temperature, weight, kl, lse, rest, flags,
+                                              sums, workspace, plan, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
+}
+
+dspark_status dspark_distill_backward(const void* draft_logits, int logits_dtype, const float* teacher_values,
+                                      const int32_t* teacher_ids, const float* rest, const float* teacher_rest,
+                                      const uint8_t* block_mask, int32_t N, int32_t gamma, int32_t V, int32_t K,
+                                      float temperature, float weight, const float* grad_scale, void* grad_draft,
+                                      void* stream) {
+  const dspark_status s = distill_sizes(logits_dtype, N, gamma, V, K, temperature);
+  if (s != DSPARK_OK || N == 0) return s;
+  if (!draft_logits || !teacher_values || !teacher_ids || !rest || !grad_draft ||
+      !aligned_to(draft_logits, logits_dtype) || !aligned_to(grad_draft, logits_dtype))
+    return DSPARK_EINVAL;
+  const size_t bytes = static_cast<size_t>(N) * gamma * V * logit_bytes(logits_dtype);
+  if (overlap(draft_logits, bytes, grad_draft, bytes)) return DSPARK_EINVAL;
+  const hipError_t e = dspark::launch_distill_backward(
+      draft_logits, logits_dtype, teacher_values, teacher_ids, rest, teacher_rest, block_mask, N, gamma, V, K,
+      temperature, weight, grad_scale, grad_draft, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
+}
+
+dspark_status dspark_beam_select(const void* logits, int logits_dtype, const float* scores, const uint8_t* finished,
+                                 int32_t eos_token, int32_t B, int32_t W, int32_t V, int32_t M, int32_t* tokens,
+                                 int32_t* parents, float* out_scores, uint8_t* flags, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (B < 0 || W <= 0 || V <= 0 || M <= 0) return DSPARK_EINVAL;
+  if (logits_dtype != DSPARK_BF16 && logits_dtype != DSPARK_F32) return DSPARK_EDTYPE;
+  if (W > DSPARK_MAX_BEAMS || M > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB ||
+      static_cast<int64_t>(B) * W > 0x7fffffffLL)
+    return DSPARK_ESHAPE;
+  if (B == 0) return DSPARK_OK;
+  if (!logits || !scores || !tokens || !parents || !out_scores || !flags || !aligned_to(logits, logits_dtype) ||
+      out_scores == scores)
+    return DSPARK_EINVAL;
+  if (finished && (eos_token < 0 || eos_token >= V)) return DSPARK_EINVAL;
+  const dspark::BeamPlan plan = dspark::plan_beam(B, W, V, M);
+  if (!workspace || workspace_bytes < plan.bytes) return DSPARK_EWORKSPACE;
+  const hipError_t e = dspark::launch_beam_select(logits, logits_dtype, scores, finished, eos_token, B, W, V, M,
+                                                  tokens, parents, out_scores, flags, workspace, plan,
+                                                  static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
+}
+
+dspark_status dspark_beam_reorder(const void* src, void* dst, const int32_t* parents, const int32_t* lengths,
+                                  int64_t L, int32_t B, int32_t W, int32_t M, int32_t S, int32_t T,
+                                  int64_t token_bytes, void* stream) {
+  if (L < 0 || B < 0 || W < 0 || M < 0 || S < 0 || T < 0 || token_bytes < 0) return DSPARK_EINVAL;
+  if (L == 0 || B == 0 || W == 0 || M == 0 || S == 0 || T == 0 || token_bytes == 0) return DSPARK_OK;
+  if (!src || !dst || !parents) return DSPARK_EINVAL;
+  // a size that no device memory holds, and with it every overflow below
+  const double row = static_cast<double>(S) * T * static_cast<double>(token_bytes);
+  if (static_cast<double>(L) * B * std::max(W, M) * row > 0x1p50) return DSPARK_ESHAPE;
+  if (src == dst) {
+    if (M != W) return DSPARK_EINVAL;
+    if (W > DSPARK_MAX_BEAMS) return DSPARK_ESHAPE;
+  } else {
+    const size_t bytes = static_cast<size_t>(L) * B * S * T * static_cast<size_t>(token_bytes);
+    if (overlap(src, bytes * W, dst, bytes * M)) return DSPARK_EINVAL;
+  }
+  const hipError_t e = dspark::launch_beam_reorder(src, dst, parents, lengths, L, B, W, M, S, T, token_bytes,
                                                    static_cast<hipStream_t>(stream));
   return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
 }

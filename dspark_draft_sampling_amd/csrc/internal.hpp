@@ -152,6 +152,60 @@ hipError_t launch_verify(const void* target, int dtype, const int32_t* draft, co
 hipError_t launch_select_width(const float* confidence, const float* cost, int32_t B, int32_t gamma,
                                int32_t* n_draft, float* expected, hipStream_t st);
 
+// ---- highest logits of rows (top.hip) ----
+struct Mass;  // rowstream.hpp
+
+// fp32 and 64-bit log2(e) / T.
+float mass_scale(float temperature);
+double mass_scale64(float temperature);
+
+// How a row is cut: P segments; G groups per thread (0: one wave a row).
+struct TopSplit {
+  int G, P;
+};
+struct TopPlan {
+  int P;  // most segments of a row
+  size_t off_parts, bytes;
+};
+TopPlan plan_top(int32_t R, int32_t V, int32_t K);
+hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, float temperature, float* values,
+                      int32_t* ids, float* rest, float* lse, uint8_t* flags, void* ws, const TopPlan& pl,
+                      hipStream_t st);
+// The lists beam selection starts from: per row and segment the K best keys
+// and the mass of the others; rows of dead and ended beams are skipped.
+int top_lists_segments(int dtype, int32_t R, int32_t V, const void* logits);
+hipError_t launch_top_lists(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, const float* scores,
+                            const uint8_t* finished, uint64_t* keys, Mass* parts, hipStream_t st);
+hipError_t launch_top_lists_merge(const uint64_t* keys, const Mass* parts, int32_t R, int32_t K, int32_t P,
+                                  const float* scores, const uint8_t* finished, uint64_t* out_keys, Mass* out_parts,
+                                  hipStream_t st);
+
+// ---- distillation from a teacher's highest logits (distill.hip) ----
+struct DistillPlan {
+  size_t off_ticket, off_partial, off_parts, bytes;
+};
+DistillPlan plan_distill(int32_t N, int32_t gamma, int32_t V);
+hipError_t launch_distill(const void* draft, int dtype, const float* values, const int32_t* ids,
+                          const float* teacher_rest, const uint8_t* block_mask, int32_t N, int32_t gamma, int32_t V,
+                          int32_t K, float temperature, float weight, float* kl, float* lse, float* rest,
+                          uint8_t* flags, float* sums, void* ws, const DistillPlan& pl, hipStream_t st);
+hipError_t launch_distill_backward(const void* draft, int dtype, const float* values, const int32_t* ids,
+                                   const float* rest, const float* teacher_rest, const uint8_t* block_mask, int32_t N,
+                                   int32_t gamma, int32_t V, int32_t K, float temperature, float weight,
+                                   const float* grad_scale, void* grad_draft, hipStream_t st);
+
+// ---- beam search (beam.hip) ----
+struct BeamPlan {
+  int P;
+  size_t off_keys, off_parts, off_mkeys, off_mparts, bytes;
+};
+BeamPlan plan_beam(int32_t B, int32_t W, int32_t V, int32_t M);
+hipError_t launch_beam_select(const void* logits, int dtype, const float* scores, const uint8_t* finished, int32_t eos,
+                              int32_t B, int32_t W, int32_t V, int32_t M, int32_t* tokens, int32_t* parents,
+                              float* out_scores, uint8_t* flags, void* ws, const BeamPlan& pl, hipStream_t st);
+hipError_t launch_beam_reorder(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L,
+                               int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t bytes, hipStream_t st);
+
 hipError_t launch_markov(const void* backbone, int dtype, const int32_t* anchor,
                          const uint16_t* w1, const uint16_t* w2, const uint16_t* hidden,
                          const uint16_t* embed, const float* conf_w, dspark_policy pol,

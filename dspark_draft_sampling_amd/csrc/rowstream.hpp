@@ -1,0 +1,225 @@
+// rowstream.hpp — device helpers of the kernels that stream one logits row at
+// a time (top.hip, beam.hip, distill.hip): 16-byte granules of a row at any
+// alignment, log-sum-exp masses, order keys and workgroup counting.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace dspark {
+
+// ---- granules ------------------------------------------------------------------
+// A row of V elements is read in 16-byte granules of the address space:
+// granule q holds the row's elements q EPL - head + [0, EPL), where head is
+// the number of elements between the 16-byte boundary at or below the row's
+// start and the start itself.  Interior granules are one 16-byte load; the
+// first and last ones, which may hold other rows' elements, are read element
+// by element, so nothing outside the row is touched at any alignment.
+template <typename T>
+struct Row {
+  static constexpr int EPL = 16 / static_cast<int>(sizeof(T));
+  const T* p;  // element 0
+  int head;    // elements before it in its granule
+  int V;
+  int Q;       // granules
+};
+
+template <typename T>
+__device__ __forceinline__ Row<T> make_row(const T* p, int V) {
+  Row<T> r;
+  r.p = p;
+  r.head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+  r.V = V;
+  r.Q = (r.head + V + Row<T>::EPL - 1) / Row<T>::EPL;
+  return r;
+}
+
+// Element j of a granule.
+__device__ __forceinline__ float gran_elem(const uint4& u, int j, uint16_t) {
+  const uint32_t w = (j >> 1) == 0 ? u.x : (j >> 1) == 1 ? u.y : (j >> 1) == 2 ? u.z : u.w;
+  return (j & 1) ? bf_hi(w) : bf_lo(w);
+}
+__device__ __forceinline__ float gran_elem(const uint4& u, int j, float) {
+  return __uint_as_float(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
+}
+
+// Granule q, elements outside the row as -inf.
+template <typename T>
+__device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
+  constexpr int EPL = Row<T>::EPL;
+  const int e0 = q * EPL - r.head;
+  if (e0 >= 0 && e0 + EPL <= r.V) return *reinterpret_cast<const uint4*>(r.p + e0);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const int e = e0 + 2 * i;
+      const uint32_t a = (e >= 0 && e < r.V) ? r.p[e] : 0xFF80u;
+      const uint32_t b = (e + 1 >= 0 && e + 1 < r.V) ? r.p[e + 1] : 0xFF80u;
+      w[i] = a | (b << 16);
+    } else {
+      const int e = e0 + i;
+      w[i] = (e >= 0 && e < r.V) ? __float_as_uint(r.p[e]) : 0xFF800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// L granules per thread, q0 + i NT + tid: one branch on the whole group (uniform)
+// keeps the interior loads free of per-lane checks.
+template <typename T, int NT, int L>
+__device__ __forceinline__ void group_load(const Row<T>& r, int q0, int tid, uint4 (&u)[L]) {
+  constexpr int EPL = Row<T>::EPL;
+  if ((q0 > 0 || r.head == 0) && (q0 + NT * L) * EPL - r.head <= r.V) {
+    const T* p = r.p + (static_cast<ptrdiff_t>(q0 + tid) * EPL - r.head);
+#pragma unroll
+    for (int i = 0; i < L; ++i) u[i] = *reinterpret_cast<const uint4*>(p + i * NT * EPL);
+  } else {
+#pragma unroll
+    for (int i = 0; i < L; ++i) u[i] = gran_load(r, q0 + i * NT + tid);
+  }
+}
+
+// ---- masses ----------------------------------------------------------------------
+// A mass is sum exp(x / T) held as (m, s): s = sum 2^(x c - fl(m c)), with m
+// the largest x, c = fl(log2(e) / T) and fl the rounding to fp32 (one fused
+// multiply-add and one exponential per element).  Values beyond kHugeLogit,
+// where m c could overflow, take s = sum 2^((x - m) c) instead.  s = 0: empty;
+// a NaN or +inf among the x makes s a NaN.
+constexpr float kHugeLogit = 1e30f;
+
+struct Mass {
+  float m;
+  float s;
+};
+
+__device__ __forceinline__ Mass mass_none() { return Mass{neg_inf(), 0.0f}; }
+
+// Exponent by which a mass relative to m becomes one relative to n >= m.
+// The products are rounded by themselves, as in the sums.
+__device__ __forceinline__ float mass_gap(float m, float n, float c) {
+#pragma clang fp contract(off)
+  return fabsf(n) > kHugeLogit || fabsf(m) > kHugeLogit ? (m - n) * c : m * c - n * c;
+}
+
+__device__ __forceinline__ Mass mass_add(Mass a, Mass b, float c) {
+  const float n = fmaxf(a.m, b.m);
+  if (n == neg_inf()) return Mass{n, a.s + b.s};  // 0, or the NaN of either
+  return Mass{n, a.s * __builtin_amdgcn_exp2f(mass_gap(a.m, n, c)) + b.s * __builtin_amdgcn_exp2f(mass_gap(b.m, n, c))};
+}
+
+// Mass of L granules held by one thread.
+template <typename T, int L>
+__device__ __forceinline__ Mass group_mass(const uint4 (&u)[L], float c) {
+  constexpr int EPL = Row<T>::EPL;
+  float m = neg_inf();
+#pragma unroll
+  for (int i = 0; i < L; ++i)
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) m = fmaxf(m, gran_elem(u[i], j, T{}));
+  float s = 0.0f;
+  if (__any(fabsf(m) > kHugeLogit && m > neg_inf())) {
+    const float ref = m > neg_inf() ? m : 0.0f;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const float x = gran_elem(u[i], j, T{});
+        s += __builtin_amdgcn_exp2f(fabsf(ref) > kHugeLogit ? (x - ref) * c : fmaf(x, c, -(ref * c)));
+      }
+  } else {
+    const float r = m > neg_inf() ? m * c : 0.0f;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s += __builtin_amdgcn_exp2f(fmaf(gran_elem(u[i], j, T{}), c, -r));
+  }
+  return Mass{m, s};
+}
+
+// log2 of a mass in 64 bits, with c64 = log2(e) / T: the rounding of m c that s
+// carries is taken out again.
+__device__ __forceinline__ double mass_log2(Mass a, float c, double c64) {
+  if (!(a.s > 0.0f) || a.m == neg_inf()) return a.s == 0.0f ? -__builtin_inf() : __builtin_nan("");
+  const double m = static_cast<double>(a.m);
+  const double fix = fabsf(a.m) > kHugeLogit ? 0.0 : static_cast<double>(a.m * c) - m * static_cast<double>(c);
+  return m * c64 + fix + log2(static_cast<double>(a.s));
+}
+
+// log2(2^a + 2^b).
+__device__ __forceinline__ double log2_add(double a, double b) {
+  const double n = fmax(a, b);
+  if (n == -__builtin_inf()) return a + b;  // -inf, or a NaN
+  return n + log2(exp2(a - n) + exp2(b - n));
+}
+
+__device__ __forceinline__ Mass wave_mass(Mass a, float c) {
+  const float n = wave_max(a.m);
+  const float k = n == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(mass_gap(a.m, n, c));
+  return Mass{n, wave_sum(a.s * k)};
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// ---- order keys --------------------------------------------------------------------
+// Unsigned keys in the order of the values (-0 as +0).  A candidate's 64-bit
+// key also orders equal values by the lower index; keys of one row are unique.
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t cand_key(uint32_t okey, int32_t index) {
+  return (static_cast<uint64_t>(okey) << 32) | static_cast<uint32_t>(~index);
+}
+__device__ __forceinline__ int32_t key_index(uint64_t k) { return static_cast<int32_t>(~static_cast<uint32_t>(k)); }
+__device__ __forceinline__ float key_value(uint64_t k) { return key_value(static_cast<uint32_t>(k >> 32)); }
+
+// Sum of a per-wave count over the workgroup, on every thread.  slots: 2 NW
+// ints, used in turn by `step`, so that one barrier a call is enough.
+template <int NW>
+__device__ __forceinline__ int block_count(int wave_count, int* slots, int step) {
+  if constexpr (NW == 1) {
+    return wave_count;
+  } else {
+    int* s = slots + (step & 1) * NW;
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = wave_count;
+    __syncthreads();
+    int t = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t += s[w];
+    return t;
+  }
+}
+
+// Largest-first threshold by bisection: a key t with want <= count(>= t) <=
+// most, or the largest t with count(>= t) >= want where no such t exists.
+// lo: a key with count(>= lo) >= want, n_lo its count; hi: one with count(>=
+// hi) < want.  count(t) must be the same on every thread.  On return n_lo is
+// count(>= t).
+template <typename Key, class Count>
+__device__ __forceinline__ Key bisect(Key lo, Key hi, int& n_lo, int want, int most, Count&& count) {
+  while (n_lo > most && hi - lo > 1) {
+    const Key mid = lo + (hi - lo) / 2;
+    const int n = count(mid);
+    if (n >= want) {
+      lo = mid;
+      n_lo = n;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+}  // namespace dspark

@@ -2,7 +2,8 @@
  * dspark.h — C ABI of the DSpark per-step sampling and verification engine
  * (MI355X / gfx950).
  *
- * Three hot-path calls:
+ * Three hot-path calls (further ones, for training, beam search and the draft
+ * width, follow them below):
  *   dspark_markov_sample  left-to-right low-rank Markov head: turns the parallel
  *                         draft backbone's block logits into gamma proposals,
  *                         their full proposal distributions q and their
@@ -176,6 +177,12 @@ enum {
 #define DSPARK_MAX_HIDDEN 65536  /* d                                */
 #define DSPARK_MAX_VOCAB (1 << 30)
 #define DSPARK_MAX_VERIFY_BATCH 65535  /* B of dspark_verify (one grid row each) */
+#define DSPARK_MAX_TOP 128       /* K of dspark_top_logits and dspark_distill, M of
+                                    dspark_beam_select                           */
+#define DSPARK_MAX_TOP_VOCAB 2097152  /* V of dspark_top_logits and
+                                         dspark_beam_select                      */
+#define DSPARK_MAX_BEAMS 32      /* W of dspark_beam_select, and of
+                                    dspark_beam_reorder in place                 */
 
 /* ---- per-request sampling policy: all DEVICE arrays of length B ----------- */
 typedef struct dspark_policy {
@@ -197,11 +204,16 @@ enum {
   DSPARK_OP_VERIFY = 2,
   DSPARK_OP_STATS = 3,
   DSPARK_OP_STATS_BACKWARD = 4,
-  DSPARK_OP_STATS_MARKOV = 5
+  DSPARK_OP_STATS_MARKOV = 5,
+  DSPARK_OP_TOP = 6,
+  DSPARK_OP_DISTILL = 7,
+  DSPARK_OP_BEAM = 8
 };
 
 /* Bytes of device workspace one call of `op` needs at these sizes (for
- * DSPARK_OP_STATS pass N as B; r and d are ignored where they do not apply).
+ * DSPARK_OP_STATS and DSPARK_OP_DISTILL pass N as B; for DSPARK_OP_TOP R as B,
+ * 1 as gamma and K as r; for DSPARK_OP_BEAM W as gamma and M as r; r and d are
+ * ignored where they do not apply).
  * Returns 0 for an unknown op or non-positive sizes.  Host-only. */
 size_t dspark_workspace_size(int op, int32_t B, int32_t gamma, int32_t V,
                              int32_t r, int32_t d);
@@ -545,6 +557,175 @@ dspark_status dspark_accept_stats_backward(
 dspark_status dspark_select_width(const float* confidence, const float* cost,
                                   int32_t B, int32_t gamma, int32_t* n_draft,
                                   float* expected, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_top_logits
+ *
+ * The K highest logits of each row, with the mass of the others: what a
+ * teacher pass keeps of its rows for dspark_distill, and what a server returns
+ * beside a token.  With z = logits / T, per row:
+ *   top_values, top_ids  the K largest logits (not divided by T) in descending
+ *                        order and their tokens; the lower token first among
+ *                        equal logits.  Tokens at -inf are no candidates:
+ *                        missing entries are -inf and -1.
+ *   rest                 log sum exp(z_v) over the tokens not listed (-inf if
+ *                        there are none above -inf), summed over those tokens
+ *                        themselves: accurate however small it is beside the top
+ *   lse                  log sum exp(z_v) over the row
+ * Inputs : logits [R, V] logits_dtype; temperature T, a host scalar.
+ * Outputs: top_values [R, K] fp32, top_ids [R, K] int32, rest, lse [R] fp32,
+ *          flags [R] uint8 (NONFINITE: the row holds a NaN or +inf, its values
+ *          are -inf, its tokens -1, rest and lse NaN; EMPTY_ROW).
+ * Workspace: dspark_workspace_size(DSPARK_OP_TOP, R, 1, V, K, 0) (0 is valid
+ * when it returns 0).
+ * Errors: EINVAL (NULL pointer, R < 0, V or K <= 0, logits not aligned to
+ * their type, T outside [2^-20, 2^20]), EDTYPE, ESHAPE (K > DSPARK_MAX_TOP, V >
+ * DSPARK_MAX_TOP_VOCAB), EWORKSPACE, EDEVICE.  K may exceed V.  R = 0 is a
+ * no-op.
+ * ------------------------------------------------------------------------- */
+dspark_status dspark_top_logits(const void* logits, int logits_dtype, int32_t R,
+                                int32_t V, int32_t K, float temperature,
+                                float* top_values, int32_t* top_ids, float* rest,
+                                float* lse, uint8_t* flags, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_distill
+ *
+ * Distillation from a teacher's highest logits, in the block form and under
+ * the loss contract of dspark_accept_stats: the draft is trained towards the K
+ * tokens that the teacher lists and, where its remaining mass is given,
+ * towards that mass as one more outcome.  Per block b and position k (row k-1),
+ * with x the draft row and j = 0..K-1:
+ *   t_j = exp(teacher_values[j] / T) / Zt,   t_r = exp(teacher_rest) / Zt,
+ *         Zt the sum of all of them (teacher_rest NULL: t_r = 0, the listed
+ *         tokens are renormalised)
+ *   s_j = exp(x[teacher_ids[j]] / T) / Zs,   s_r = sum over the tokens not
+ *         listed of exp(x_v / T) / Zs,       Zs = sum_v exp(x_v / T)
+ *   kl  = sum_j t_j (log t_j - log s_j) + t_r (log t_r - log s_r),
+ *         0 log 0 = 0; +inf where the draft excludes what the teacher keeps
+ * with w_k = exp(-k/gamma), mask_b = block_mask[b] != 0:
+ *   sums[0] numerator  = weight sum_b mask_b sum_k w_k kl
+ *   sums[1] num_tokens = gamma sum_b mask_b
+ *   sums[2..3] report pair of kl [sum, count] over masked positions.
+ * A caller that wants the usual T^2 passes it in weight.
+ *
+ * Inputs
+ *   draft_logits   [N, gamma, V] logits_dtype
+ *   teacher_values [N, gamma, K] fp32, teacher_ids [N, gamma, K] int32: as
+ *                  written by dspark_top_logits (any order).  An entry whose
+ *                  token is outside [0, V) is none; a token listed twice is two
+ *                  outcomes with the same s_j, and is counted once in Zs.
+ *   teacher_rest   [N, gamma] fp32 (`rest` of dspark_top_logits at the same T)
+ *                  or NULL
+ *   block_mask     [N] uint8 or NULL (all ones)
+ *   temperature    T, weight: host scalars
+ * Outputs
+ *   kl    [N, gamma] fp32 (every block, masked or not)
+ *   lse   [N, gamma] fp32: log Zs
+ *   rest  [N, gamma] fp32: log of the draft's mass outside the list (-inf if
+ *         none); dspark_distill_backward reads it
+ *   flags [N, gamma] uint8: NONFINITE (a NaN or +inf in the row, the listed
+ *         values or teacher_rest: kl, lse and rest are NaN), EMPTY_ROW (no
+ *         draft logit above -inf, or no teacher outcome with mass: kl is 0)
+ *   sums  [4] fp32
+ * Workspace: dspark_workspace_size(DSPARK_OP_DISTILL, N, gamma, V, 0, 0).
+ * Errors: EINVAL (NULL pointer, N < 0, a size <= 0, misaligned logits, T
+ * outside [2^-20, 2^20]), EDTYPE, ESHAPE (gamma, V ranges, K >
+ * DSPARK_MAX_TOP, N gamma >= 2^31), EWORKSPACE, EDEVICE.  N = 0 writes zero
+ * sums.
+ * ------------------------------------------------------------------------- */
+dspark_status dspark_distill(const void* draft_logits, int logits_dtype,
+                             const float* teacher_values,
+                             const int32_t* teacher_ids,
+                             const float* teacher_rest,
+                             const uint8_t* block_mask, int32_t N, int32_t gamma,
+                             int32_t V, int32_t K, float temperature,
+                             float weight, float* kl, float* lse, float* rest,
+                             uint8_t* flags, float* sums, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_distill_backward
+ *
+ * The gradient of grad_scale * sums[0] of dspark_distill (same inputs) into
+ * the draft logits; the teacher's side is detached:
+ *   grad[v] = (grad_scale weight mask_b w_k / T) d_v
+ *   d_v = s_v - sum_{j: teacher_ids[j] = v} t_j               for listed v
+ *   d_v = (s_r - t_r) exp(x_v / T) / sum_{u not listed} exp(x_u / T)  otherwise
+ * The row's normaliser is formed again, in 64 bits, from `rest` and the draft's
+ * logits at the listed tokens.  Rows of masked blocks and rows flagged
+ * EMPTY_ROW are zeros; rows flagged NONFINITE are NaN or unspecified.
+ *
+ * Inputs : as dspark_distill; rest [N, gamma] as it wrote it; grad_scale device
+ *          float32 scalar or NULL (1).
+ * Outputs: grad_draft [N, gamma, V] in logits_dtype (bf16: rounded to nearest
+ *          even).  It must not overlap draft_logits (EINVAL).
+ * No workspace.  Errors: as dspark_distill.  N = 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+dspark_status dspark_distill_backward(
+    const void* draft_logits, int logits_dtype, const float* teacher_values,
+    const int32_t* teacher_ids, const float* rest, const float* teacher_rest,
+    const uint8_t* block_mask, int32_t N, int32_t gamma, int32_t V, int32_t K,
+    float temperature, float weight, const float* grad_scale, void* grad_draft,
+    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_beam_select
+ *
+ * One step of a beam search over the full vocabulary: of a request's beams w
+ * and tokens v the M candidates with the highest
+ *   scores[b, w] + logits[b, w, v] - logsumexp(logits[b, w, :])
+ * in descending order.  The sums are formed and compared in 64 bits; equal ones
+ * go by the lower beam, then the higher logit, then the lower token.
+ *   A beam with finished[b, w] != 0 is one candidate, (eos_token, its score);
+ *   its logits are not read.  A beam whose score is -inf is none (in the first
+ *   step of a search all beams but one are so); its logits are not read.
+ *   Tokens at -inf are no candidates.  Where there are fewer than M candidates
+ *   the remaining picks are token -1, parent -1, score -inf.
+ * Inputs : logits [B, W, V] logits_dtype; scores [B, W] fp32: the beams' sums of
+ *          log-probabilities; finished [B, W] uint8 or NULL (none); eos_token,
+ *          read only with finished.
+ * Outputs: tokens, parents [B, M] int32, out_scores [B, M] fp32 (the 64-bit sums
+ *          rounded); flags [B, W] uint8: NONFINITE (a NaN or +inf among the
+ *          logits read or as the score: the beam gives no candidate), EMPTY_ROW
+ *          (all logits read are -inf).  out_scores must not be scores.
+ * Workspace: dspark_workspace_size(DSPARK_OP_BEAM, B, W, V, M, 0).
+ * Errors: EINVAL (NULL pointer, B < 0, a size <= 0, misaligned logits,
+ * eos_token outside [0, V) with finished given, out_scores == scores), EDTYPE,
+ * ESHAPE (W > DSPARK_MAX_BEAMS, M > DSPARK_MAX_TOP, V > DSPARK_MAX_TOP_VOCAB,
+ * B W >= 2^31), EWORKSPACE, EDEVICE.  B = 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+dspark_status dspark_beam_select(const void* logits, int logits_dtype,
+                                 const float* scores, const uint8_t* finished,
+                                 int32_t eos_token, int32_t B, int32_t W,
+                                 int32_t V, int32_t M, int32_t* tokens,
+                                 int32_t* parents, float* out_scores,
+                                 uint8_t* flags, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_beam_reorder
+ *
+ * Beam states (caches, token histories) moved to the beams that a selection
+ * kept, as bytes:
+ *   dst[l, b, j, s, t, :] = src[l, b, parents[b, j], s, t, :]
+ * for l < L, b < B, j < M, s < S and t < lengths[b] (clamped into [0, T]; NULL:
+ * T), each token `token_bytes` bytes.  src is [L, B, W, S, T, token_bytes], dst
+ * [L, B, M, S, T, token_bytes].  Everything else of dst is left as it was: the
+ * tokens at and after a request's length, and the rows of beams whose parent is
+ * outside [0, W) (a pick that is none).  dst may be src (M = W, at most
+ * DSPARK_MAX_BEAMS): the states are then exchanged in place, and beams that
+ * are their own parent are not touched.  Other overlaps are EINVAL.
+ * No workspace.  Errors: EINVAL (NULL src, dst or parents, a size < 0, partial
+ * overlap, in place with M != W), ESHAPE (in place with W > DSPARK_MAX_BEAMS),
+ * EDEVICE.  Any size of 0 makes it a no-op.
+ * ------------------------------------------------------------------------- */
+dspark_status dspark_beam_reorder(const void* src, void* dst,
+                                  const int32_t* parents, const int32_t* lengths,
+                                  int64_t L, int32_t B, int32_t W, int32_t M,
+                                  int32_t S, int32_t T, int64_t token_bytes,
+                                  void* stream);
 
 #ifdef __cplusplus
 }
