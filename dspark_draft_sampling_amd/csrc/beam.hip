@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kFinalThreads = 256;
 constexpr int kFinalWaves = kFinalThreads / 64;
-constexpr int kMaxCand = DSPARK_MAX_BEAMS * DSPARK_MAX_TOP;  // candidates of a request
+constexpr int kMaxCand = 5632;  // candidates of a request: DSPARK_MAX_BEAMS lists of the longest length fit
 constexpr int kMaxGrid = 1 << 20;
 constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kLog2ed = 1.4426950408889634074;
@@ -43,7 +43,7 @@ constexpr uint64_t kKey64NegInf = 0x000FFFFFFFFFFFFFull;
 struct BeamArgs {
   const float* scores;
   const uint8_t* finished;  // or NULL
-  int32_t eos, B, W, M, E;  // E: candidates listed per beam (segments x M)
+  int32_t eos, B, W, M, E;  // E: list entries per beam
   int32_t P;                // masses per beam
   int32_t* tokens;
   int32_t* parents;
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
   __shared__ uint16_t sh_list[kMaxCand];
   __shared__ double sh_lse[DSPARK_MAX_BEAMS];
   __shared__ uint8_t sh_state[DSPARK_MAX_BEAMS];  // 0: none, 1: live, 2: ended
-  __shared__ int slots[2 * NW];
+  __shared__ int slots[6 * NW];
   __shared__ int nlist;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int n = a.W * a.E;
@@ -133,18 +133,22 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
       }
       found += __popcll(__ballot(d > -__builtin_inf()));
     }
-    found = block_count<NW>(found, slots, step++);  // its barrier completes sh_score
-    if constexpr (NW == 1) __syncthreads();
+    found = block_count<NW>(Count3{found, 0, 0}, slots, step).a;  // its barrier completes sh_score
     // ---- those that can be among the M ----
     uint64_t bound = kKey64NegInf + 1;
     const int most = a.M + a.M / 4 + 8;
     if (found > std::max(most, 64)) {
       int n_lo = found;
-      bound = bisect<uint64_t>(bound, order_key64(__builtin_inf()) + 1, n_lo, a.M, most, [&](uint64_t mid) {
-        int k = 0;
-        for (int i = tid; i < (n + 63) / 64 * 64; i += NT)
-          k += __popcll(__ballot(i < n && order_key64(sh_score[min(i, n - 1)]) >= mid));
-        return block_count<NW>(k, slots, step++);
+      bound = search_key<uint64_t>(bound, order_key64(__builtin_inf()) + 1, n_lo, a.M, most,
+                                   [&](uint64_t t1, uint64_t t2, uint64_t t3) {
+        Count3 k{0, 0, 0};
+        for (int i = tid; i < (n + 63) / 64 * 64; i += NT) {
+          const uint64_t d = i < n ? order_key64(sh_score[i]) : 0;
+          k.a += __popcll(__ballot(d >= t1));
+          k.b += __popcll(__ballot(d >= t2));
+          k.c += __popcll(__ballot(d >= t3));
+        }
+        return block_count<NW>(k, slots, step);
       });
     }
     for (int i = tid; i < n; i += NT)
@@ -267,12 +271,12 @@ BeamPlan plan_beam(int32_t B, int32_t W, int32_t V, int32_t M) {
   const size_t rp = static_cast<size_t>(R) * t.P;
   size_t off = 0;
   p.off_keys = off;
-  off = align_up(off + rp * M * sizeof(uint64_t), 256);
+  off = align_up(off + rp * top_list_len(M) * sizeof(uint64_t), 256);
   p.off_parts = off;
   off = align_up(off + rp * sizeof(Mass), 256);
-  if (static_cast<int64_t>(W) * M * t.P > kMaxCand) {
+  if (static_cast<int64_t>(W) * top_list_len(M) * t.P > kMaxCand) {
     p.off_mkeys = off;
-    off = align_up(off + static_cast<size_t>(R) * M * sizeof(uint64_t), 256);
+    off = align_up(off + static_cast<size_t>(R) * top_list_len(M) * sizeof(uint64_t), 256);
     p.off_mparts = off;
     off = align_up(off + static_cast<size_t>(R) * sizeof(Mass), 256);
   }
@@ -287,10 +291,10 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
   char* w = static_cast<char*>(ws);
   uint64_t* keys = reinterpret_cast<uint64_t*>(w + pl.off_keys);
   Mass* parts = reinterpret_cast<Mass*>(w + pl.off_parts);
-  int P = top_lists_segments(dtype, R, V, logits);
+  int P = top_lists_segments(dtype, R, V, M, logits);
   hipError_t e = launch_top_lists(logits, dtype, R, V, M, scores, finished, keys, parts, st);
   if (e != hipSuccess) return e;
-  if (static_cast<int64_t>(W) * M * P > kMaxCand) {
+  if (static_cast<int64_t>(W) * top_list_len(M) * P > kMaxCand) {
     uint64_t* mkeys = reinterpret_cast<uint64_t*>(w + pl.off_mkeys);
     Mass* mparts = reinterpret_cast<Mass*>(w + pl.off_mparts);
     e = launch_top_lists_merge(keys, parts, R, M, P, scores, finished, mkeys, mparts, st);
@@ -299,7 +303,7 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
     parts = mparts;
     P = 1;
   }
-  const BeamArgs a{scores, finished, eos, B, W, M, P * M, P, tokens, parents, out_scores, flags};
+  const BeamArgs a{scores, finished, eos, B, W, M, P * top_list_len(M), P, tokens, parents, out_scores, flags};
   DSPARK_LAUNCH("beam_final", beam_final_kernel, dim3(static_cast<unsigned>(std::min(B, kMaxGrid))),
                 dim3(kFinalThreads), 0, st, keys, parts, mass_scale(1.0f), mass_scale64(1.0f), a);
   return hipGetLastError();

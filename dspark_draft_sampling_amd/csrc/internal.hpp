@@ -159,9 +159,9 @@ struct Mass;  // rowstream.hpp
 float mass_scale(float temperature);
 double mass_scale64(float temperature);
 
-// How a row is cut: P segments; G groups per thread (0: one wave a row).
+// How a row is cut: P segments of `groups` groups a thread, workgroups of NT.
 struct TopSplit {
-  int G, P;
+  int NT, groups, P;
 };
 struct TopPlan {
   int P;  // most segments of a row
@@ -171,9 +171,10 @@ TopPlan plan_top(int32_t R, int32_t V, int32_t K);
 hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, float temperature, float* values,
                       int32_t* ids, float* rest, float* lse, uint8_t* flags, void* ws, const TopPlan& pl,
                       hipStream_t st);
-// The lists beam selection starts from: per row and segment the K best keys
-// and the mass of the others; rows of dead and ended beams are skipped.
-int top_lists_segments(int dtype, int32_t R, int32_t V, const void* logits);
+// The lists beam selection starts from: per row and segment K or a few
+// more of its best keys, in no order, and the mass of the others; rows of dead and ended beams are skipped.
+int top_lists_segments(int dtype, int32_t R, int32_t V, int32_t K, const void* logits);
+int top_list_len(int K);  // keys of a segment's list (0: none)
 hipError_t launch_top_lists(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, const float* scores,
                             const uint8_t* finished, uint64_t* keys, Mass* parts, hipStream_t st);
 hipError_t launch_top_lists_merge(const uint64_t* keys, const Mass* parts, int32_t R, int32_t K, int32_t P,

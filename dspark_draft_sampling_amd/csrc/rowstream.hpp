@@ -139,20 +139,23 @@ __device__ __forceinline__ Mass group_mass(const uint4 (&u)[L], float c) {
   return Mass{m, s};
 }
 
-// log2 of a mass in 64 bits, with c64 = log2(e) / T: the rounding of m c that s
-// carries is taken out again.
+// log2 of a mass, with c64 = log2(e) / T: the rounding of m c that s carries is
+// taken out again.  The terms are added in 64 bits; the logarithm of s is one
+// of 32 bits on its mantissa, off by less than 2^-23 (the sum itself is no better).
 __device__ __forceinline__ double mass_log2(Mass a, float c, double c64) {
+#pragma clang fp contract(off)
   if (!(a.s > 0.0f) || a.m == neg_inf()) return a.s == 0.0f ? -__builtin_inf() : __builtin_nan("");
   const double m = static_cast<double>(a.m);
   const double fix = fabsf(a.m) > kHugeLogit ? 0.0 : static_cast<double>(a.m * c) - m * static_cast<double>(c);
-  return m * c64 + fix + log2(static_cast<double>(a.s));
+  const float lg = __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(a.s));  // log2
+  return m * c64 + fix + (static_cast<double>(lg) + static_cast<double>(__builtin_amdgcn_frexp_expf(a.s)));
 }
 
-// log2(2^a + 2^b).
+// log2(2^a + 2^b), the sum's logarithm in 32 bits (it lies in [0, 1]).
 __device__ __forceinline__ double log2_add(double a, double b) {
-  const double n = fmax(a, b);
+  const double n = fmax(a, b), d = fmin(a, b);
   if (n == -__builtin_inf()) return a + b;  // -inf, or a NaN
-  return n + log2(exp2(a - n) + exp2(b - n));
+  return n + static_cast<double>(__builtin_amdgcn_logf(1.0f + __builtin_amdgcn_exp2f(static_cast<float>(d - n))));
 }
 
 __device__ __forceinline__ Mass wave_mass(Mass a, float c) {
@@ -185,38 +188,89 @@ __device__ __forceinline__ uint64_t cand_key(uint32_t okey, int32_t index) {
 __device__ __forceinline__ int32_t key_index(uint64_t k) { return static_cast<int32_t>(~static_cast<uint32_t>(k)); }
 __device__ __forceinline__ float key_value(uint64_t k) { return key_value(static_cast<uint32_t>(k >> 32)); }
 
-// Sum of a per-wave count over the workgroup, on every thread.  slots: 2 NW
-// ints, used in turn by `step`, so that one barrier a call is enough.
+// Exclusive prefix sum over the workgroup's threads, and the total.  slots: NW
+// ints, free again after the next barrier.
 template <int NW>
-__device__ __forceinline__ int block_count(int wave_count, int* slots, int step) {
-  if constexpr (NW == 1) {
-    return wave_count;
-  } else {
-    int* s = slots + (step & 1) * NW;
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = wave_count;
-    __syncthreads();
-    int t = 0;
+__device__ __forceinline__ int block_scan(int v, int* slots, int& total) {
+  const int lane = threadIdx.x & 63;
+  int inc = v;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) t += s[w];
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(inc, d, 64);
+    if (lane >= d) inc += up;
+  }
+  const int all = lane_i(inc, 63);
+  if constexpr (NW == 1) {
+    total = all;
+    return inc - v;
+  } else {
+    const int wave = threadIdx.x >> 6;
+    if (lane == 0) slots[wave] = all;
+    __syncthreads();
+    int base = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      base += w < wave ? slots[w] : 0;
+      total += slots[w];
+    }
+    return base + inc - v;
+  }
+}
+
+// Three per-wave counts summed over the workgroup, on every thread.  slots: 6
+// NW ints, used in turn by `step`, so that one barrier a call is enough.
+struct Count3 {
+  int a, b, c;
+};
+template <int NW>
+__device__ __forceinline__ Count3 block_count(Count3 n, int* slots, int& step) {
+  if constexpr (NW == 1) {
+    return n;
+  } else {
+    int* s = slots + (step++ & 1) * 3 * NW;
+    if ((threadIdx.x & 63) == 0) {
+      s[threadIdx.x >> 6] = n.a;
+      s[NW + (threadIdx.x >> 6)] = n.b;
+      s[2 * NW + (threadIdx.x >> 6)] = n.c;
+    }
+    __syncthreads();
+    Count3 t{0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      t.a += s[w];
+      t.b += s[NW + w];
+      t.c += s[2 * NW + w];
+    }
     return t;
   }
 }
 
-// Largest-first threshold by bisection: a key t with want <= count(>= t) <=
-// most, or the largest t with count(>= t) >= want where no such t exists.
-// lo: a key with count(>= lo) >= want, n_lo its count; hi: one with count(>=
-// hi) < want.  count(t) must be the same on every thread.  On return n_lo is
-// count(>= t).
+// Largest-first threshold by a search in quarters: a key t with want <=
+// count(>= t) <= most, or the largest t with count(>= t) >= want where no such t
+// exists.  lo: a key with count(>= lo) = n_lo >= want; hi: one with count(>= hi)
+// < want.  count(t1, t2, t3), t1 <= t2 <= t3, gives the counts of keys at or above
+// each, the same on every thread.  On return n_lo is count(>= t).
 template <typename Key, class Count>
-__device__ __forceinline__ Key bisect(Key lo, Key hi, int& n_lo, int want, int most, Count&& count) {
+__device__ __forceinline__ Key search_key(Key lo, Key hi, int& n_lo, int want, int most, Count&& count) {
   while (n_lo > most && hi - lo > 1) {
-    const Key mid = lo + (hi - lo) / 2;
-    const int n = count(mid);
-    if (n >= want) {
-      lo = mid;
-      n_lo = n;
+    const Key d = hi - lo;
+    const Key t1 = lo + max(d / 4, static_cast<Key>(1)), t2 = lo + max(d / 2, static_cast<Key>(1));
+    const Key t3 = lo + max(d / 4 + d / 2, static_cast<Key>(1));
+    const Count3 n = count(t1, t2, t3);
+    if (n.c >= want) {
+      lo = t3;
+      n_lo = n.c;
+    } else if (n.b >= want) {
+      lo = t2;
+      n_lo = n.b;
+      hi = t3;
+    } else if (n.a >= want) {
+      lo = t1;
+      n_lo = n.a;
+      hi = t2;
     } else {
-      hi = mid;
+      hi = t1;
     }
   }
   return lo;
