@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import atexit
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -467,17 +468,54 @@ def dspark_select_width(confidence, cost, want_expected=True, out=None):
     return out
 
 
-def _scratch(op, device, nbytes):
-    """Workspace of one call.  Outside a stream capture it is the cached one of
-    (device, stream, op).  A captured call gets memory of its graph's own pool:
-    a graph keeps using the address, so a buffer that eager calls share and may
-    replace by a larger one would not do, nor one that two graphs share."""
-    if nbytes == 0:
-        return None, 0
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
-    ws = _workspace(op, device, nbytes)
-    return ws, ws.numel()
+class _on:
+    """The launch context of one call: its device is the current one inside (and
+    only switched to if it is not), stream is the device's current stream."""
+
+    __slots__ = ("device", "stream", "_guard")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        d = self.device
+        self._guard = None
+        if torch.cuda.current_device() != d.index:
+            self._guard = torch.cuda.device(d)
+            self._guard.__enter__()
+        self.stream = torch.cuda.current_stream(d).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+    def scratch(self, op, *sizes):
+        """(address, bytes) of the call's workspace.  Outside a stream capture
+        it is the cached one of (device, stream, op).  A captured call gets memory
+        of its graph's own pool: a graph keeps using the address, so a buffer that
+        eager calls share and may replace by a larger one would not do, nor one
+        that two graphs share."""
+        nbytes = _need(op, *sizes)
+        if nbytes == 0:
+            return None, 0
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            return ws.data_ptr(), nbytes
+        ws = _ws.get((self.device, self.stream, op))
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspace(op, self.device, nbytes)
+        return ws.data_ptr(), ws.numel()
+
+
+@functools.lru_cache(maxsize=1024)
+def _need(op, *sizes):
+    return dspark_workspace_size(op, *sizes)
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
 
 
 def _outputs(what, spec, out, device):
@@ -508,14 +546,14 @@ def dspark_top_logits(logits, k, temperature=1.0, out=None):
     if R > 0x7fffffff or V > 0x7fffffff:
         raise DSparkError("top_logits: logits have too many rows or tokens")
     dev = logits.device
-    with torch.cuda.device(dev):
+    with _on(dev) as c:
         out = _outputs("top_logits", [("top_values", torch.float32, (*lead, k)),
                                       ("top_ids", torch.int32, (*lead, k)), ("rest", torch.float32, lead),
                                       ("lse", torch.float32, lead), ("flags", torch.uint8, lead)], out, dev)
-        ws, nb = _scratch(DSPARK_OP_TOP, dev, dspark_workspace_size(DSPARK_OP_TOP, R, 1, V, k))
-        rc = lib().dspark_top_logits(_p(logits), dt, R, V, k, float(temperature), _p(out["top_values"]),
-                                     _p(out["top_ids"]), _p(out["rest"]), _p(out["lse"]),
-                                     _p(out["flags"]), _p(ws), nb, _stream(dev))
+        ws, nb = c.scratch(DSPARK_OP_TOP, R, 1, V, k)
+        rc = lib().dspark_top_logits(_a(logits), dt, R, V, k, float(temperature), _a(out["top_values"]),
+                                     _a(out["top_ids"]), _a(out["rest"]), _a(out["lse"]),
+                                     _a(out["flags"]), ws, nb, c.stream)
     _check(rc)
     return out
 
@@ -549,15 +587,15 @@ def dspark_distill(draft, teacher_values, teacher_ids, teacher_rest=None, block_
     kl, lse, rest [N, gamma] f32, flags [N, gamma] uint8 and sums [4] f32."""
     dt, N, g, V, K = _distill_args("distill", draft, teacher_values, teacher_ids, teacher_rest, block_mask)
     dev = draft.device
-    with torch.cuda.device(dev):
+    with _on(dev) as c:
         out = _outputs("distill", [("kl", torch.float32, (N, g)), ("lse", torch.float32, (N, g)),
                                    ("rest", torch.float32, (N, g)), ("flags", torch.uint8, (N, g)),
                                    ("sums", torch.float32, (4,))], out, dev)
-        ws, nb = _scratch(DSPARK_OP_DISTILL, dev, dspark_workspace_size(DSPARK_OP_DISTILL, N, g, V))
-        rc = lib().dspark_distill(_p(draft), dt, _p(teacher_values), _p(teacher_ids), _p(teacher_rest),
-                                  _p(block_mask), N, g, V, K, float(temperature), float(weight),
-                                  _p(out["kl"]), _p(out["lse"]), _p(out["rest"]), _p(out["flags"]),
-                                  _p(out["sums"]), _p(ws), nb, _stream(dev))
+        ws, nb = c.scratch(DSPARK_OP_DISTILL, N, g, V)
+        rc = lib().dspark_distill(_a(draft), dt, _a(teacher_values), _a(teacher_ids), _a(teacher_rest),
+                                  _a(block_mask), N, g, V, K, float(temperature), float(weight),
+                                  _a(out["kl"]), _a(out["lse"]), _a(out["rest"]), _a(out["flags"]),
+                                  _a(out["sums"]), ws, nb, c.stream)
     _check(rc)
     return out
 
@@ -576,12 +614,12 @@ def dspark_distill_backward(draft, teacher_values, teacher_ids, rest, teacher_re
         _dev_tensor(grad_scale, torch.float32, "grad_scale", device=dev)
         if grad_scale.numel() != 1:
             raise DSparkError("distill_backward: grad_scale must hold one value")
-    with torch.cuda.device(dev):
+    with _on(dev) as c:
         out = _outputs("distill_backward", [("grad_draft", draft.dtype, (N, g, V))], out, dev)
-        rc = lib().dspark_distill_backward(_p(draft), dt, _p(teacher_values), _p(teacher_ids), _p(rest),
-                                           _p(teacher_rest), _p(block_mask), N, g, V, K,
-                                           float(temperature), float(weight), _p(grad_scale),
-                                           _p(out["grad_draft"]), _stream(dev))
+        rc = lib().dspark_distill_backward(_a(draft), dt, _a(teacher_values), _a(teacher_ids), _a(rest),
+                                           _a(teacher_rest), _a(block_mask), N, g, V, K,
+                                           float(temperature), float(weight), _a(grad_scale),
+                                           _a(out["grad_draft"]), c.stream)
     _check(rc)
     return out
 
@@ -604,14 +642,14 @@ def dspark_beam_select(logits, scores, picks, finished=None, eos_token=0, out=No
     _dev_tensor(scores, torch.float32, "scores", (B, W), dev)
     if finished is not None:
         _dev_tensor(finished, torch.uint8, "finished", (B, W), dev)
-    with torch.cuda.device(dev):
+    with _on(dev) as c:
         out = _outputs("beam_select", [("tokens", torch.int32, (B, M)), ("parents", torch.int32, (B, M)),
                                        ("scores", torch.float32, (B, M)), ("flags", torch.uint8, (B, W))],
                        out, dev)
-        ws, nb = _scratch(DSPARK_OP_BEAM, dev, dspark_workspace_size(DSPARK_OP_BEAM, B, W, V, M))
-        rc = lib().dspark_beam_select(_p(logits), dt, _p(scores), _p(finished), int(eos_token), B, W, V, M,
-                                      _p(out["tokens"]), _p(out["parents"]), _p(out["scores"]),
-                                      _p(out["flags"]), _p(ws), nb, _stream(dev))
+        ws, nb = c.scratch(DSPARK_OP_BEAM, B, W, V, M)
+        rc = lib().dspark_beam_select(_a(logits), dt, _a(scores), _a(finished), int(eos_token), B, W, V, M,
+                                      _a(out["tokens"]), _a(out["parents"]), _a(out["scores"]),
+                                      _a(out["flags"]), ws, nb, c.stream)
     _check(rc)
     return out
 
@@ -657,13 +695,13 @@ def dspark_beam_reorder(state, parents, batch_dim=0, lengths=None, length_dim=No
     shape = (*state.shape[:d + 1], M, *state.shape[d + 2:])
     if max(B, W, M, S, T) > 0x7fffffff:
         raise DSparkError("beam_reorder: a dimension is too large")
-    with torch.cuda.device(dev):
+    with _on(dev) as c:
         if out is None:
             out = torch.zeros(shape, dtype=state.dtype, device=dev)
         else:
             _dev_tensor(out, state.dtype, "out", shape, dev)
-        rc = lib().dspark_beam_reorder(_p(state), _p(out), _p(parents), _p(lengths), outer, B, W, M, S, T,
-                                       inner * state.element_size(), _stream(dev))
+        rc = lib().dspark_beam_reorder(_a(state), _a(out), _a(parents), _a(lengths), outer, B, W, M, S, T,
+                                       inner * state.element_size(), c.stream)
     _check(rc)
     return out
 

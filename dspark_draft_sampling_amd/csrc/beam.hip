@@ -5,15 +5,13 @@
 // best of score_w + x_v - lse_w over a request's live beams w and tokens v.
 //
 // Selection: a beam's M best tokens hold all that the request can take from
-// it, so the rows go through the pass of top.hip (each live beam's M highest
-// logits and the mass of the others, one read of the row); ended and dead
-// beams are not read.  beam_final, one workgroup a request, forms each beam's
-// normaliser in 64 bits (the listed tokens one by one, the others as their
-// 32-bit mass) and every candidate's score in 64 bits: candidates of two beams
-// can stand closer than 32 bits tell apart.  Few candidates are ranked by
-// counting at once; of many, a bisection over the scores' order keys keeps M
-// or a few more first.  Equal scores go by beam, logit and token, so the
-// order is total and does not depend on timing.
+// it, so the rows go through the pass of top.hip (one read of each live beam's
+// row; ended and dead beams are not read), which leaves per beam a list with its
+// M best candidates and their scores in 64 bits: candidates of two beams can
+// stand closer than 32 bits tell apart.  beam_final, one workgroup a request,
+// ranks them: a candidate's rank is the number of better ones; of many, a search
+// over the scores' order keys keeps M or a few more first.  Equal scores go by
+// beam, logit and token, so the order is total and does not depend on timing.
 //
 // Reordering: a copy.  A thread moves the same 16 bytes of every beam of a
 // request, all loads before all stores, so a parent with several children is
@@ -29,121 +27,62 @@ namespace {
 
 constexpr int kFinalThreads = 256;
 constexpr int kFinalWaves = kFinalThreads / 64;
-constexpr int kMaxCand = 5632;  // candidates of a request: DSPARK_MAX_BEAMS lists of the longest length fit
+constexpr int kMaxCand = 5376;  // DSPARK_MAX_BEAMS lists of the longest length
+constexpr int kRankAll = 128;   // candidates ranked at once; more are first cut by a search
 constexpr int kMaxGrid = 1 << 20;
-constexpr double kLn2d = 0.69314718055994530942;
-constexpr double kLog2ed = 1.4426950408889634074;
 
-__device__ __forceinline__ uint64_t order_key64(double x) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
-}
-constexpr uint64_t kKey64NegInf = 0x000FFFFFFFFFFFFFull;
-
-struct BeamArgs {
-  const float* scores;
-  const uint8_t* finished;  // or NULL
-  int32_t eos, B, W, M, E;  // E: list entries per beam
-  int32_t P;                // masses per beam
-  int32_t* tokens;
-  int32_t* parents;
-  float* out_scores;
-  uint8_t* flags;
-};
-
-__global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ keys,
-                                                                   const Mass* __restrict__ parts, float c, double c64,
-                                                                   BeamArgs a) {
+__global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ sums,
+                                                                   const uint64_t* __restrict__ keys, int32_t B,
+                                                                   int32_t W, int32_t M, int32_t E,
+                                                                   int32_t* __restrict__ tokens,
+                                                                   int32_t* __restrict__ parents,
+                                                                   float* __restrict__ scores) {
   constexpr int NT = kFinalThreads, NW = kFinalWaves;
-  __shared__ double sh_score[kMaxCand];
-  __shared__ uint16_t sh_list[kMaxCand];
-  __shared__ double sh_lse[DSPARK_MAX_BEAMS];
-  __shared__ uint8_t sh_state[DSPARK_MAX_BEAMS];  // 0: none, 1: live, 2: ended
+  __shared__ uint64_t sh_sum[kMaxCand + 4];
+  __shared__ uint64_t sh_best[kMaxCand + 4];
+  __shared__ uint16_t sh_from[kMaxCand];
   __shared__ int slots[6 * NW];
-  __shared__ int nlist;
+  __shared__ int scan[2][NW];
+  __shared__ uint64_t red[2][NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  const int n = a.W * a.E;
+  const int n = W * E;
   int step = 0;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    // ---- the beams' normalisers ----
-    for (int w = wave; w < a.W; w += NW) {
-      const size_t row = static_cast<size_t>(b) * a.W + w;
-      const float sc = a.scores[row];
-      const bool ended = a.finished && a.finished[row] != 0;
-      uint8_t state = 0, flag = 0;
-      double lse = 0.0;
-      if (isnan(sc) || sc == pos_inf()) {
-        flag = DSPARK_FLAG_NONFINITE;
-      } else if (sc > neg_inf()) {
-        if (ended) {
-          state = 2;
-        } else {
-          Mass m = mass_none();
-          for (int p = lane; p < a.P; p += 64) m = mass_add(m, parts[row * a.P + p], c);
-          m = wave_mass(m, c);
-          if (!(m.s >= 0.0f)) {
-            flag = DSPARK_FLAG_NONFINITE;
-          } else {
-            const double others = mass_log2(m, c, c64);
-            float top = neg_inf();
-            for (int i = lane; i < a.E; i += 64) {
-              const uint64_t k = keys[row * a.E + i];
-              if (k) top = fmaxf(top, key_value(k));
-            }
-            top = wave_max(top);
-            if (top == neg_inf()) {
-              flag = DSPARK_FLAG_EMPTY_ROW;
-            } else {
-              const double ref = static_cast<double>(top);
-              double s = 0.0;
-              for (int i = lane; i < a.E; i += 64) {
-                const uint64_t k = keys[row * a.E + i];
-                if (k) s += exp2((static_cast<double>(key_value(k)) - ref) * kLog2ed);
-              }
-              s = wave_sum64(s) + exp2(others - ref * kLog2ed);
-              lse = ref + log2(s) * kLn2d;
-              state = 1;
-            }
-          }
-        }
-      }
-      if (lane == 0) {
-        sh_lse[w] = lse;
-        sh_state[w] = state;
-        a.flags[row] = flag;
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    const uint64_t* key = keys + static_cast<size_t>(b) * n;
+    // ---- the candidates that there are, in order ----
+    uint64_t top = 0, low = ~0ull;
+    int mine = 0, found;
+    for (int i = tid; i < n; i += NT) {
+      const uint64_t d = sums[static_cast<size_t>(b) * n + i];
+      sh_sum[i] = d;
+      if (d > kKey64NegInf) {
+        ++mine;
+        top = max(top, d);
+        low = min(low, d);
       }
     }
-    if (tid == 0) nlist = 0;
-    __syncthreads();
-    // ---- the candidates' scores ----
-    int found = 0;
-    for (int i = tid; i < (n + 63) / 64 * 64; i += NT) {
-      double d = -__builtin_inf();
-      if (i < n) {
-        const int w = i / a.E, e = i - w * a.E;
-        const size_t row = static_cast<size_t>(b) * a.W + w;
-        const uint8_t state = sh_state[w];
-        if (state == 1) {
-          const uint64_t k = keys[row * a.E + e];
-          if (k) d = static_cast<double>(a.scores[row]) + (static_cast<double>(key_value(k)) - sh_lse[w]);
-        } else if (state == 2 && e == 0) {
-          d = static_cast<double>(a.scores[row]);
-        }
-        sh_score[i] = d;
-      }
-      found += __popcll(__ballot(d > -__builtin_inf()));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
+      low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
     }
-    found = block_count<NW>(Count3{found, 0, 0}, slots, step).a;  // its barrier completes sh_score
-    // ---- those that can be among the M ----
+    if (lane == 0) {
+      red[0][wave] = top;
+      red[1][wave] = low;
+    }
+    block_scan<NW>(mine, scan[0], found);  // its barrier completes sh_sum and red
     uint64_t bound = kKey64NegInf + 1;
-    const int most = a.M + a.M / 4 + 8;
-    if (found > std::max(most, 64)) {
+    if (found > kRankAll) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        top = max(top, red[0][w]);
+        low = min(low, red[1][w]);
+      }
       int n_lo = found;
-      bound = search_key<uint64_t>(bound, order_key64(__builtin_inf()) + 1, n_lo, a.M, most,
-                                   [&](uint64_t t1, uint64_t t2, uint64_t t3) {
+      bound = search_key<uint64_t>(low, top + 1, n_lo, M, M + M / 4 + 8, [&](uint64_t t1, uint64_t t2, uint64_t t3) {
         Count3 k{0, 0, 0};
         for (int i = tid; i < (n + 63) / 64 * 64; i += NT) {
-          const uint64_t d = i < n ? order_key64(sh_score[i]) : 0;
+          const uint64_t d = i < n ? sh_sum[i] : 0;
           k.a += __popcll(__ballot(d >= t1));
           k.b += __popcll(__ballot(d >= t2));
           k.c += __popcll(__ballot(d >= t3));
@@ -151,39 +90,48 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
         return block_count<NW>(k, slots, step);
       });
     }
+    // ---- those that can be among the M ----
+    int nb;
+    mine = 0;
+    for (int i = tid; i < n; i += NT) mine += sh_sum[i] >= bound;
+    int pos = block_scan<NW>(mine, scan[1], nb);
     for (int i = tid; i < n; i += NT)
-      if (order_key64(sh_score[i]) >= bound) sh_list[atomicAdd(&nlist, 1)] = static_cast<uint16_t>(i);
+      if (sh_sum[i] >= bound) {
+        sh_best[pos] = sh_sum[i];
+        sh_from[pos++] = static_cast<uint16_t>(i);
+      }
+    if (tid < 4) sh_best[nb + tid] = 0;
     __syncthreads();
     // ---- rank: score, then beam, logit, token ----
-    const int nl = nlist;
-    const size_t base = static_cast<size_t>(b) * a.W;
-    for (int i = tid; i < nl; i += NT) {
-      const int ci = sh_list[i], w = ci / a.E;
-      const double d = sh_score[ci];
-      const uint64_t k = sh_state[w] == 1 ? keys[base * a.E + ci] : 0;
-      int rank = 0;
-      for (int j = 0; j < nl; ++j) {
-        const int cj = sh_list[j];
-        const double dj = sh_score[cj];
-        if (dj > d) {
-          ++rank;
-        } else if (dj == d && cj != ci) {
-          const int wj = cj / a.E;
-          if (wj < w || (wj == w && keys[base * a.E + cj] > k)) ++rank;
-        }
+    for (int i = tid; i < nb; i += NT) {
+      const uint64_t d = sh_best[i];
+      int rank = 0, same = 0;
+      for (int j = 0; j < nb; j += 4) {
+        const uint64_t d0 = sh_best[j], d1 = sh_best[j + 1], d2 = sh_best[j + 2], d3 = sh_best[j + 3];
+        rank += (d0 > d) + (d1 > d) + (d2 > d) + (d3 > d);
+        same += (d0 == d) + (d1 == d) + (d2 == d) + (d3 == d);
       }
-      if (rank < a.M) {
-        const size_t o = static_cast<size_t>(b) * a.M + rank;
-        a.tokens[o] = k ? key_index(k) : a.eos;
-        a.parents[o] = w;
-        a.out_scores[o] = static_cast<float>(d);
+      if (rank >= M) continue;
+      const int from = sh_from[i], w = from / E;
+      const uint64_t k = key[from];
+      if (same > 1)
+        for (int j = 0; j < nb; ++j)
+          if (j != i && sh_best[j] == d) {
+            const int wj = sh_from[j] / E;
+            rank += wj < w || (wj == w && key[sh_from[j]] > k);
+          }
+      if (rank < M) {
+        const size_t o = static_cast<size_t>(b) * M + rank;
+        tokens[o] = key_index(k);
+        parents[o] = w;
+        scores[o] = static_cast<float>(key_double(d));
       }
     }
-    for (int j = found + tid; j < a.M; j += NT) {  // fewer candidates than picks
-      const size_t o = static_cast<size_t>(b) * a.M + j;
-      a.tokens[o] = -1;
-      a.parents[o] = -1;
-      a.out_scores[o] = neg_inf();
+    for (int j = found + tid; j < M; j += NT) {  // fewer candidates than picks
+      const size_t o = static_cast<size_t>(b) * M + j;
+      tokens[o] = -1;
+      parents[o] = -1;
+      scores[o] = neg_inf();
     }
     __syncthreads();  // LDS is reused by the next request
   }
@@ -261,51 +209,32 @@ hipError_t move(const void* src, void* dst, const int32_t* parents, const int32_
 
 }  // namespace
 
-// Keys and masses of the beams' segments; where a request's lists would not
-// fit beam_final, the beams' merged ones too.
 BeamPlan plan_beam(int32_t B, int32_t W, int32_t V, int32_t M) {
   BeamPlan p{};
   const int32_t R = B * W;
-  const TopPlan t = plan_top(R, V, M);
-  p.P = t.P;
-  const size_t rp = static_cast<size_t>(R) * t.P;
+  p.rows = plan_top(R, V, M);
+  const size_t list = static_cast<size_t>(R) * top_list_len(M) * sizeof(uint64_t);
   size_t off = 0;
+  p.off_sums = off;
+  off = align_up(off + list, 256);
   p.off_keys = off;
-  off = align_up(off + rp * top_list_len(M) * sizeof(uint64_t), 256);
-  p.off_parts = off;
-  off = align_up(off + rp * sizeof(Mass), 256);
-  if (static_cast<int64_t>(W) * top_list_len(M) * t.P > kMaxCand) {
-    p.off_mkeys = off;
-    off = align_up(off + static_cast<size_t>(R) * top_list_len(M) * sizeof(uint64_t), 256);
-    p.off_mparts = off;
-    off = align_up(off + static_cast<size_t>(R) * sizeof(Mass), 256);
-  }
-  p.bytes = off;
+  off = align_up(off + list, 256);
+  p.off_rows = off;
+  p.bytes = align_up(off + p.rows.bytes, 256);
   return p;
 }
 
 hipError_t launch_beam_select(const void* logits, int dtype, const float* scores, const uint8_t* finished, int32_t eos,
                               int32_t B, int32_t W, int32_t V, int32_t M, int32_t* tokens, int32_t* parents,
                               float* out_scores, uint8_t* flags, void* ws, const BeamPlan& pl, hipStream_t st) {
-  const int32_t R = B * W;
   char* w = static_cast<char*>(ws);
+  uint64_t* sums = reinterpret_cast<uint64_t*>(w + pl.off_sums);
   uint64_t* keys = reinterpret_cast<uint64_t*>(w + pl.off_keys);
-  Mass* parts = reinterpret_cast<Mass*>(w + pl.off_parts);
-  int P = top_lists_segments(dtype, R, V, M, logits);
-  hipError_t e = launch_top_lists(logits, dtype, R, V, M, scores, finished, keys, parts, st);
+  const hipError_t e = launch_beam_rows(logits, dtype, B * W, V, M, scores, finished, eos, sums, keys, flags,
+                                        w + pl.off_rows, pl.rows, st);
   if (e != hipSuccess) return e;
-  if (static_cast<int64_t>(W) * top_list_len(M) * P > kMaxCand) {
-    uint64_t* mkeys = reinterpret_cast<uint64_t*>(w + pl.off_mkeys);
-    Mass* mparts = reinterpret_cast<Mass*>(w + pl.off_mparts);
-    e = launch_top_lists_merge(keys, parts, R, M, P, scores, finished, mkeys, mparts, st);
-    if (e != hipSuccess) return e;
-    keys = mkeys;
-    parts = mparts;
-    P = 1;
-  }
-  const BeamArgs a{scores, finished, eos, B, W, M, P * top_list_len(M), P, tokens, parents, out_scores, flags};
   DSPARK_LAUNCH("beam_final", beam_final_kernel, dim3(static_cast<unsigned>(std::min(B, kMaxGrid))),
-                dim3(kFinalThreads), 0, st, keys, parts, mass_scale(1.0f), mass_scale64(1.0f), a);
+                dim3(kFinalThreads), 0, st, sums, keys, B, W, M, top_list_len(M), tokens, parents, out_scores);
   return hipGetLastError();
 }
 

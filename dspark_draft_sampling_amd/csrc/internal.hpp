@@ -171,15 +171,12 @@ TopPlan plan_top(int32_t R, int32_t V, int32_t K);
 hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, float temperature, float* values,
                       int32_t* ids, float* rest, float* lse, uint8_t* flags, void* ws, const TopPlan& pl,
                       hipStream_t st);
-// The lists beam selection starts from: per row and segment K or a few
-// more of its best keys, in no order, and the mass of the others; rows of dead and ended beams are skipped.
-int top_lists_segments(int dtype, int32_t R, int32_t V, int32_t K, const void* logits);
-int top_list_len(int K);  // keys of a segment's list (0: none)
-hipError_t launch_top_lists(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, const float* scores,
-                            const uint8_t* finished, uint64_t* keys, Mass* parts, hipStream_t st);
-hipError_t launch_top_lists_merge(const uint64_t* keys, const Mass* parts, int32_t R, int32_t K, int32_t P,
-                                  const float* scores, const uint8_t* finished, uint64_t* out_keys, Mass* out_parts,
-                                  hipStream_t st);
+// Per beam a list of top_list_len(M) candidates that holds its M best: the order
+// keys of their 64-bit scores and their keys; and the beams' flags.
+int top_list_len(int K);
+hipError_t launch_beam_rows(const void* logits, int dtype, int32_t R, int32_t V, int32_t M, const float* scores,
+                            const uint8_t* finished, int32_t eos, uint64_t* sums, uint64_t* keys, uint8_t* flags,
+                            void* ws, const TopPlan& pl, hipStream_t st);
 
 // ---- distillation from a teacher's highest logits (distill.hip) ----
 struct DistillPlan {
@@ -197,8 +194,8 @@ hipError_t launch_distill_backward(const void* draft, int dtype, const float* va
 
 // ---- beam search (beam.hip) ----
 struct BeamPlan {
-  int P;
-  size_t off_keys, off_parts, off_mkeys, off_mparts, bytes;
+  TopPlan rows;
+  size_t off_sums, off_keys, off_rows, bytes;
 };
 BeamPlan plan_beam(int32_t B, int32_t W, int32_t V, int32_t M);
 hipError_t launch_beam_select(const void* logits, int dtype, const float* scores, const uint8_t* finished, int32_t eos,

@@ -164,10 +164,27 @@ __device__ __forceinline__ Mass wave_mass(Mass a, float c) {
   return Mass{n, wave_sum(a.s * k)};
 }
 
+// Sum over the wave in 64 bits, the same on every lane: DPP within each row of
+// 16 lanes, then the four row sums.
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = static_cast<uint32_t>(dpp_i<CTRL>(static_cast<int>(b)));
+  const uint32_t hi = static_cast<uint32_t>(dpp_i<CTRL>(static_cast<int>(b >> 32)));
+  return __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(hi) << 32) | lo));
+}
+__device__ __forceinline__ double lane_d(double v, int l) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = static_cast<uint32_t>(lane_i(static_cast<int>(b), l));
+  const uint32_t hi = static_cast<uint32_t>(lane_i(static_cast<int>(b >> 32), l));
+  return __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(hi) << 32) | lo));
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v += dpp_d<kDppXor1>(v);
+  v += dpp_d<kDppXor2>(v);
+  v += dpp_d<kDppHalfMirror>(v);
+  v += dpp_d<kDppMirror>(v);
+  return (lane_d(v, 0) + lane_d(v, 16)) + (lane_d(v, 32) + lane_d(v, 48));
 }
 
 // ---- order keys --------------------------------------------------------------------
@@ -187,6 +204,16 @@ __device__ __forceinline__ uint64_t cand_key(uint32_t okey, int32_t index) {
 }
 __device__ __forceinline__ int32_t key_index(uint64_t k) { return static_cast<int32_t>(~static_cast<uint32_t>(k)); }
 __device__ __forceinline__ float key_value(uint64_t k) { return key_value(static_cast<uint32_t>(k >> 32)); }
+
+// The same order for 64-bit values.
+constexpr uint64_t kKey64NegInf = 0x000FFFFFFFFFFFFFull;
+__device__ __forceinline__ uint64_t order_key(double x) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_double(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) ? k ^ 0x8000000000000000ull : ~k));
+}
 
 // Exclusive prefix sum over the workgroup's threads, and the total.  slots: NW
 // ints, free again after the next barrier.

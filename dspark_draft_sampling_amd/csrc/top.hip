@@ -38,12 +38,23 @@ namespace {
 constexpr int kMergeThreads = 256;
 constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch; each then takes several items
 constexpr int kL = 4;              // granules of a group
-constexpr int kG = 16;             // groups of a thread at most
+
+// Groups of a thread at most (they are kept in LDS) and keys that are ranked at
+// once: more are first cut by a search.
+template <int NT>
+struct TopCaps {
+  static constexpr int kG = NT == 1024 ? 8 : 16;
+  static constexpr int kRank = NT == 64 ? 128 : NT == 256 ? 512 : 1024;
+};
 
 // Candidates a list may hold beyond K: the searches stop at the first bound
 // within it.
 __host__ __device__ constexpr int list_len(int K) { return K + K / 4 + 8; }
 constexpr int kMaxList = list_len(DSPARK_MAX_TOP);
+
+// What a launch leaves: a segment's candidates and mass for the merge, a row's
+// outputs, or a beam's candidates with their scores for beam_final.
+enum TopMode { kLists, kRows, kBeams };
 
 struct TopOut {
   float* values;   // [R, K]
@@ -55,15 +66,35 @@ struct TopOut {
   Mass* parts;     // [R, P]: the mass of its other elements
 };
 
-// skip: rows (beams) that are not read at all.
-struct TopSkip {
-  const float* scores;      // NULL: none is skipped
-  const uint8_t* finished;  // or NULL
+// Beams (scores NULL: plain rows).  An ended beam is one candidate, a beam
+// whose score is not finite is none; their rows are not read.
+struct TopBeams {
+  const float* scores;      // [R]
+  const uint8_t* finished;  // [R] or NULL
+  int32_t eos;
+  uint64_t* sums;  // [R, list_len(K)]: order keys of the candidates' 64-bit scores
+  uint8_t* flags;  // [R]
 };
-__device__ __forceinline__ bool skipped(const TopSkip& s, size_t row) {
-  if (!s.scores) return false;
-  const float sc = s.scores[row];
-  return !(sc > neg_inf() && sc < pos_inf()) || (s.finished && s.finished[row]);
+
+// Whether the row is a beam that is not read; in mode kBeams its candidates
+// are written here.
+template <int NT, TopMode MODE>
+__device__ __forceinline__ bool unread_beam(const TopBeams& bm, const TopOut& o, size_t row, int K) {
+  if (MODE == kRows || !bm.scores) return false;
+  const float sc = bm.scores[row];
+  const bool ended = bm.finished && bm.finished[row];
+  if (sc > neg_inf() && sc < pos_inf() && !ended) return false;
+  if constexpr (MODE == kBeams) {
+    const bool fine = sc > neg_inf() && sc < pos_inf();
+    const int len = list_len(K);
+    for (int j = threadIdx.x; j < len; j += NT) {
+      const bool one = fine && j == 0;
+      bm.sums[row * len + j] = order_key(one ? static_cast<double>(sc) : -__builtin_inf());
+      o.keys[row * len + j] = one ? cand_key(0, bm.eos) : 0;
+    }
+    if (threadIdx.x == 0) bm.flags[row] = isnan(sc) || sc == pos_inf() ? DSPARK_FLAG_NONFINITE : 0;
+  }
+  return true;
 }
 
 // A key with K <= count(>= it) <= list_len(K) among n distinct keys in LDS (0:
@@ -87,20 +118,21 @@ __device__ __forceinline__ uint64_t list_bound(const uint64_t* cand, int n, int 
   });
 }
 
-// The K best of n <= kMaxList distinct keys in LDS in descending order into
-// sorted[0, K) (0 where there are fewer).  list is padded to a multiple of 4
-// with 0.  Complete on return.
+// The K best of n distinct keys in LDS in descending order into sorted[0, K) (0
+// where there are fewer), each at its rank, the number of greater keys.  keys
+// has room for 4 more; 0s among them are none.  Complete on return.
 template <int NT>
-__device__ __forceinline__ void rank_list(uint64_t* list, int n, int K, uint64_t* sorted) {
+__device__ __forceinline__ void rank_keys(uint64_t* keys, int n, int K, uint64_t* sorted) {
   const int tid = threadIdx.x;
   for (int j = tid; j < K; j += NT) sorted[j] = 0;
-  if (tid < 4) list[n + tid] = 0;
+  if (tid < 4) keys[n + tid] = 0;
   __syncthreads();
   for (int i = tid; i < n; i += NT) {
-    const uint64_t k = list[i];
+    const uint64_t k = keys[i];
+    if (k == 0) continue;
     int rank = 0;
     for (int j = 0; j < n; j += 4) {
-      const uint64_t k0 = list[j], k1 = list[j + 1], k2 = list[j + 2], k3 = list[j + 3];
+      const uint64_t k0 = keys[j], k1 = keys[j + 1], k2 = keys[j + 2], k3 = keys[j + 3];
       rank += (k0 > k) + (k1 > k) + (k2 > k) + (k3 > k);
     }
     if (rank < K) sorted[rank] = k;
@@ -132,6 +164,29 @@ __device__ __forceinline__ void write_row(const TopOut& o, size_t row, const uin
   }
 }
 
+// A beam's candidates from its n keys and the mass of its other tokens (by the
+// first wave): the normaliser in 64 bits, the listed tokens one by one.
+__device__ __forceinline__ void write_beam(const TopBeams& bm, const TopOut& o, size_t row, const uint64_t* list, int n,
+                                           int K, Mass others, bool bad, float c, double c64) {
+  const int lane = threadIdx.x, len = list_len(K);
+  if (bad) n = 0;
+  float top = neg_inf();
+  for (int j = lane; j < n; j += 64)
+    if (list[j]) top = fmaxf(top, key_value(list[j]));
+  const double ref = static_cast<double>(wave_max(top));
+  double sum = 0.0;
+  for (int j = lane; j < n; j += 64)
+    if (list[j]) sum += exp2((static_cast<double>(key_value(list[j])) - ref) * c64);
+  sum = wave_sum64(sum) + exp2(mass_log2(others, c, c64) - ref * c64);
+  const double lse = ref + log2(sum) / c64, sc = static_cast<double>(bm.scores[row]);
+  for (int j = lane; j < len; j += 64) {
+    const uint64_t k = j < n ? list[j] : 0;
+    bm.sums[row * len + j] = k ? order_key(sc + (static_cast<double>(key_value(k)) - lse)) : kKey64NegInf;
+    o.keys[row * len + j] = k;
+  }
+  if (lane == 0) bm.flags[row] = bad ? DSPARK_FLAG_NONFINITE : ref == -__builtin_inf() ? DSPARK_FLAG_EMPTY_ROW : 0;
+}
+
 // Mass of a granule's elements for which keep(value, index) holds.
 template <typename T, class F>
 __device__ __forceinline__ Mass gran_mass(const uint4& u, int e0, float c, F&& keep) {
@@ -152,9 +207,10 @@ __device__ __forceinline__ Mass gran_mass(const uint4& u, int e0, float c, F&& k
 
 template <int NT>
 struct TopLds {
+  static constexpr int kCand = TopCaps<NT>::kG * NT;
   union {
-    Mass grp[kG * NT];       // the groups
-    uint64_t cand[kG * NT];  // then the candidates
+    Mass grp[kCand];           // the groups
+    uint64_t cand[kCand + 4];  // then the candidates
   };
   uint64_t list[kMaxList + 4];
   uint64_t sorted[DSPARK_MAX_TOP];
@@ -244,22 +300,22 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
   return total;
 }
 
-template <typename T, int NT, bool FINAL>
+template <typename T, int NT, TopMode MODE>
 __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict__ logits, int64_t items, int32_t V,
                                                             int32_t K, int32_t P, int32_t groups, float c, double c64,
-                                                            TopSkip skip, TopOut o) {
+                                                            TopBeams bm, TopOut o) {
   constexpr int NW = NT / 64;
   constexpr int EPL = Row<T>::EPL;
   constexpr int TILE = NT * kL;  // granules of a group over the workgroup
   __shared__ TopLds<NT> s;
-  constexpr int QUAL = sizeof(s.qual) / sizeof(uint16_t), CAND = kG * NT;
+  constexpr int QUAL = sizeof(s.qual) / sizeof(uint16_t), CAND = TopLds<NT>::kCand;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   int step = 0;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const size_t row = static_cast<size_t>(item / P);
     const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
-    if (skipped(skip, row)) continue;
+    if (unread_beam<NT, MODE>(bm, o, row, K)) continue;
     const Row<T> r = make_row(logits + row * V, V);
     const int first = seg * groups * TILE;
     const int n = min(groups, (r.Q - first + TILE - 1) / TILE);  // <= 0: nothing left of this row
@@ -304,7 +360,8 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
     }
 
     Mass others = mass_none();
-    int nl = 0;  // candidates in s.list
+    int nl = 0;  // candidates listed
+    uint64_t* list = s.cand;
     if (!bad && wmax > neg_inf()) {
       // ---- bound: at least K threads' (or groups') maxima reach it, or all finite ones ----
       const uint32_t kmax = order_key(wmax);
@@ -399,28 +456,36 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
       if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s, step, others);
 
       // ---- the K best of them or a few more; the others' mass ----
-      const uint64_t lo = static_cast<uint64_t>(bound) << 32;
-      const uint64_t t = list_bound<NT>(s.cand, nc, nc, K, lo, static_cast<uint64_t>(kmax + 1) << 32, s.slots, step);
-      mine = 0;
-      for (int i = tid; i < nc; i += NT) mine += s.cand[i] >= t;
-      pos = block_scan<NW>(mine, s.scan[0], nl);
-      for (int i = tid; i < nc; i += NT) {
-        const uint64_t k = s.cand[i];
-        if (k >= t) {
-          s.list[pos++] = k;
-        } else {
-          others = mass_add(others, Mass{key_value(k), 1.0f}, c);
+      nl = nc;
+      if (nc > (MODE == kRows ? TopCaps<NT>::kRank : list_len(K))) {
+        const uint64_t t = list_bound<NT>(s.cand, nc, nc, K, static_cast<uint64_t>(bound) << 32,
+                                          static_cast<uint64_t>(kmax + 1) << 32, s.slots, step);
+        mine = 0;
+        for (int i = tid; i < nc; i += NT) mine += s.cand[i] >= t;
+        pos = block_scan<NW>(mine, s.scan[0], nl);
+        for (int i = tid; i < nc; i += NT) {
+          const uint64_t k = s.cand[i];
+          if (k >= t) {
+            s.list[pos++] = k;
+          } else {
+            others = mass_add(others, Mass{key_value(k), 1.0f}, c);
+          }
         }
+        __syncthreads();
+        list = s.list;
       }
-      __syncthreads();
-      if constexpr (FINAL) {
-        rank_list<NT>(s.list, nl, K, s.sorted);
+      if constexpr (MODE == kRows) {
+        rank_keys<NT>(list, nl, K, s.sorted);
         const uint64_t kth = s.sorted[K - 1];  // 0: fewer than K, all of them are in
         for (int i = tid; i < nl; i += NT)
-          if (s.list[i] < kth) others = mass_add(others, Mass{key_value(s.list[i]), 1.0f}, c);
+          if (list[i] < kth) others = mass_add(others, Mass{key_value(list[i]), 1.0f}, c);
       }
-    } else if constexpr (FINAL) {
+    } else if constexpr (MODE == kRows) {
       for (int j = tid; j < K; j += NT) s.sorted[j] = 0;
+    }
+    if constexpr (MODE == kLists) {
+      const int len = list_len(K);
+      for (int j = tid; j < len; j += NT) o.keys[(row * P + seg) * len + j] = j < nl ? list[j] : 0;
     }
 
     // ---- the segment's mass, outputs ----
@@ -432,74 +497,87 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
     } else {
       __syncthreads();
     }
-    if constexpr (FINAL) {
+    if constexpr (MODE == kRows) {
       if (wave == 0) write_row(o, row, s.sorted, K, others, bad, c, c64);
+    } else if constexpr (MODE == kBeams) {
+      if (wave == 0) write_beam(bm, o, row, list, nl, K, others, bad, c, c64);
     } else {
-      const size_t part = row * P + seg;
-      const int len = list_len(K);
-      for (int j = tid; j < len; j += NT) o.keys[part * len + j] = j < nl ? s.list[j] : 0;
-      if (tid == 0) o.parts[part] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
+      if (tid == 0) o.parts[row * P + seg] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
     }
     __syncthreads();  // LDS is reused by the next item
   }
 }
 
-// The K best of the candidates of a row's P segments, one workgroup a row.
-// FINAL: the row's outputs; otherwise its keys and mass at o.keys / o.parts as
-// one segment's.
-template <bool FINAL>
-__global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t* __restrict__ keys,
+// The K best of the candidates of a row's P segments (in: their lists), one
+// workgroup a row; kRows or kBeams.
+template <TopMode MODE>
+__global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t* __restrict__ in,
                                                                   const Mass* __restrict__ parts, int32_t R, int32_t K,
-                                                                  int32_t P, float c, double c64, TopSkip skip,
+                                                                  int32_t P, float c, double c64, TopBeams bm,
                                                                   TopOut o) {
   constexpr int NT = kMergeThreads, NW = NT / 64;
-  extern __shared__ uint64_t all[];  // P list_len(K) keys
+  extern __shared__ uint64_t all[];  // P list_len(K) keys and 4 more
   __shared__ uint64_t list[kMaxList + 4];
   __shared__ uint64_t sorted[DSPARK_MAX_TOP];
   __shared__ int slots[6 * NW];
   __shared__ int scan[2][NW];
-  __shared__ uint64_t red[NW];
+  __shared__ uint64_t red[2][NW];
   __shared__ Mass shm[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int len = list_len(K), n = P * len;
   int step = 0;
   for (int row = blockIdx.x; row < R; row += gridDim.x) {
     const size_t at = static_cast<size_t>(row);
-    if (skipped(skip, at)) continue;
-    uint64_t top = 0;
+    if (unread_beam<NT, MODE>(bm, o, at, K)) continue;
+    uint64_t top = 0, low = ~0ull;
     int found = 0;
     for (int i = tid; i < n; i += NT) {
-      const uint64_t k = keys[at * n + i];
+      const uint64_t k = in[at * n + i];
       all[i] = k;
       top = max(top, k);
+      if (k) low = min(low, k);
       found += k != 0;
     }
     Mass others = mass_none();
     for (int p = tid; p < P; p += NT) others = mass_add(others, parts[at * P + p], c);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
-    if (lane == 0) red[wave] = top;
+    for (int d = 1; d < 64; d <<= 1) {
+      top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
+      low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
+    }
+    if (lane == 0) {
+      red[0][wave] = top;
+      red[1][wave] = low;
+    }
     block_scan<NW>(found, scan[0], found);  // its barrier completes all and red
 #pragma unroll
-    for (int w = 0; w < NW; ++w) top = max(top, red[w]);
-    const uint64_t t = list_bound<NT>(all, n, found, K, 1, top + 1, slots, step);
-    int mine = 0, nl;
-    for (int i = tid; i < n; i += NT) mine += all[i] >= t;
-    int pos = block_scan<NW>(mine, scan[1], nl);
-    for (int i = tid; i < n; i += NT) {
-      const uint64_t k = all[i];
-      if (k >= t) {
-        list[pos++] = k;
-      } else if (k) {
-        others = mass_add(others, Mass{key_value(k), 1.0f}, c);
-      }
+    for (int w = 0; w < NW; ++w) {
+      top = max(top, red[0][w]);
+      low = min(low, red[1][w]);
     }
-    __syncthreads();
-    if constexpr (FINAL) {
-      rank_list<NT>(list, nl, K, sorted);
+    uint64_t* best = all;
+    int nl = n;
+    if (n > (MODE == kRows ? 2 * list_len(K) : list_len(K))) {
+      const uint64_t t = list_bound<NT>(all, n, found, K, found ? low : 1, top + 1, slots, step);
+      int mine = 0;
+      for (int i = tid; i < n; i += NT) mine += all[i] >= t;
+      int pos = block_scan<NW>(mine, scan[1], nl);
+      for (int i = tid; i < n; i += NT) {
+        const uint64_t k = all[i];
+        if (k >= t) {
+          list[pos++] = k;
+        } else if (k) {
+          others = mass_add(others, Mass{key_value(k), 1.0f}, c);
+        }
+      }
+      __syncthreads();
+      best = list;
+    }
+    if constexpr (MODE == kRows) {
+      rank_keys<NT>(best, nl, K, sorted);
       const uint64_t kth = sorted[K - 1];
       for (int i = tid; i < nl; i += NT)
-        if (list[i] < kth) others = mass_add(others, Mass{key_value(list[i]), 1.0f}, c);
+        if (best[i] != 0 && best[i] < kth) others = mass_add(others, Mass{key_value(best[i]), 1.0f}, c);
     }
     others = wave_mass(others, c);
     if (lane == 0) shm[wave] = others;
@@ -507,65 +585,77 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
     if (wave == 0) {
       others = wave_mass(lane < NW ? shm[lane] : mass_none(), c);
       const bool bad = !(others.s >= 0.0f);
-      if constexpr (FINAL) {
+      if constexpr (MODE == kRows)
         write_row(o, at, sorted, K, others, bad, c, c64);
-      } else {
-        for (int j = lane; j < len; j += 64) o.keys[at * len + j] = j < nl ? list[j] : 0;
-        if (lane == 0) o.parts[at] = others;
-      }
+      else
+        write_beam(bm, o, at, best, nl, K, others, bad, c, c64);
     }
     __syncthreads();
   }
 }
 
 // Rows are cut into segments of `groups` groups a thread.  Many short rows are
-// taken by a wave each; others by workgroups of 256 threads, in shorter segments
-// where that is needed to fill the GPU.
-TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
+// taken by a wave each; many rows by workgroups of 256 threads, of which several
+// share a compute unit; few rows by workgroups of 1024.
+TopSplit top_split(int epl, int64_t R, int32_t V, bool any) {
   // granules of a row, at the least favourable alignment
   const int q = any ? (V + 2 * epl - 2) / epl : V / epl;
   TopSplit s{};
-  const int wave = 64 * kL, block = 256 * kL;
-  if (q <= 2 * wave || (q <= kG * wave && R >= 4096)) {
+  int most;
+  if (q <= 2 * 64 * kL || (q <= TopCaps<64>::kG * 64 * kL && R >= 4096)) {
     s.NT = 64;
-    s.groups = (q + wave - 1) / wave;
-    s.P = 1;
-    return s;
+    most = TopCaps<64>::kG;
+  } else if (q <= 2 * 256 * kL || R >= 1024) {
+    s.NT = 256;
+    most = TopCaps<256>::kG;
+  } else {
+    s.NT = 1024;
+    most = TopCaps<1024>::kG;
   }
-  s.NT = 256;
-  int g = std::min(kG, (q + block - 1) / block);
-  // every segment's list goes through the merge's LDS
-  const int most = 56 * 1024 / (list_len(K) * static_cast<int>(sizeof(uint64_t)));
-  while (g > 1 && R * ((q + block * g - 1) / (block * g)) < 512) {
-    const int h = g / 2;
-    if ((q + block * h - 1) / (block * h) > most) break;
-    g = h;
-  }
-  s.groups = g;
-  s.P = (q + block * g - 1) / (block * g);
+  const int need = (q + s.NT * kL - 1) / (s.NT * kL);  // groups of a thread over the row
+  s.P = (need + most - 1) / most;
+  s.groups = (need + s.P - 1) / s.P;
   return s;
 }
 
-template <typename T, bool FINAL>
+template <typename T, TopMode MODE>
 hipError_t launch_segments(const T* logits, int32_t R, int32_t V, int32_t K, const TopSplit& sp, float c, double c64,
-                           TopSkip skip, TopOut o, hipStream_t st) {
+                           const TopBeams& bm, const TopOut& o, hipStream_t st) {
   const int64_t items = static_cast<int64_t>(R) * sp.P;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid)));
+#define DSPARK_TOP(NT)                                                                                              \
+  DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, NT, MODE>), grid, dim3(NT), 0, st, logits, items, V, K, sp.P, \
+                sp.groups, c, c64, bm, o)
   if (sp.NT == 64)
-    DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, 64, FINAL>), grid, dim3(64), 0, st, logits, items, V, K, sp.P,
-                  sp.groups, c, c64, skip, o);
+    DSPARK_TOP(64);
+  else if (sp.NT == 256)
+    DSPARK_TOP(256);
   else
-    DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, 256, FINAL>), grid, dim3(256), 0, st, logits, items, V, K, sp.P,
-                  sp.groups, c, c64, skip, o);
+    DSPARK_TOP(1024);
+#undef DSPARK_TOP
   return hipGetLastError();
 }
 
-template <bool FINAL>
-hipError_t launch_merge(const uint64_t* keys, const Mass* parts, int32_t R, int32_t K, int32_t P, float c, double c64,
-                        TopSkip skip, TopOut o, hipStream_t st) {
-  DSPARK_LAUNCH("top_merge", (top_merge_kernel<FINAL>), dim3(static_cast<unsigned>(std::min(R, kMaxGrid))),
-                dim3(kMergeThreads), static_cast<size_t>(P) * list_len(K) * sizeof(uint64_t), st, keys, parts, R, K, P,
-                c, c64, skip, o);
+// The segments' candidates, then (rows of several segments) the merge.
+template <TopMode MODE>
+hipError_t launch_rows(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, const TopSplit& sp,
+                       float temperature, const TopBeams& bm, TopOut o, uint64_t* lists, Mass* parts, hipStream_t st) {
+  const float c = mass_scale(temperature);
+  const double c64 = mass_scale64(temperature);
+  const uint16_t* h = static_cast<const uint16_t*>(logits);
+  const float* f = static_cast<const float*>(logits);
+  if (sp.P == 1)
+    return dtype == DSPARK_BF16 ? launch_segments<uint16_t, MODE>(h, R, V, K, sp, c, c64, bm, o, st)
+                                : launch_segments<float, MODE>(f, R, V, K, sp, c, c64, bm, o, st);
+  TopOut part = o;
+  part.keys = lists;
+  part.parts = parts;
+  const hipError_t e = dtype == DSPARK_BF16 ? launch_segments<uint16_t, kLists>(h, R, V, K, sp, c, c64, bm, part, st)
+                                            : launch_segments<float, kLists>(f, R, V, K, sp, c, c64, bm, part, st);
+  if (e != hipSuccess) return e;
+  DSPARK_LAUNCH("top_merge", (top_merge_kernel<MODE>), dim3(static_cast<unsigned>(std::min(R, kMaxGrid))),
+                dim3(kMergeThreads), (static_cast<size_t>(sp.P) * list_len(K) + 4) * sizeof(uint64_t), st, lists, parts,
+                R, K, sp.P, c, c64, bm, o);
   return hipGetLastError();
 }
 
@@ -585,7 +675,7 @@ TopPlan plan_top(int32_t R, int32_t V, int32_t K) {
   int P = 1;
   for (const int epl : {4, 8})
     for (const bool any : {false, true})
-      if (any || V % epl == 0) P = std::max(P, top_split(epl, R, V, K, any).P);
+      if (any || V % epl == 0) P = std::max(P, top_split(epl, R, V, any).P);
   p.P = P;
   const size_t rp = static_cast<size_t>(R) * P;
   size_t off = 0;
@@ -602,53 +692,21 @@ hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32
                       int32_t* ids, float* rest, float* lse, uint8_t* flags, void* ws, const TopPlan& pl,
                       hipStream_t st) {
   const int epl = dtype == DSPARK_BF16 ? 8 : 4;
-  const TopSplit sp = top_split(epl, R, V, K, any_alignment(logits, V, epl));
-  const float c = mass_scale(temperature);
-  const double c64 = mass_scale64(temperature);
   char* w = static_cast<char*>(ws);
-  TopOut o{values, ids, rest, lse, flags, nullptr, nullptr};
-  const TopSkip none{nullptr, nullptr};
-  if (sp.P == 1) {
-    if (dtype == DSPARK_BF16)
-      return launch_segments<uint16_t, true>(static_cast<const uint16_t*>(logits), R, V, K, sp, c, c64, none, o, st);
-    return launch_segments<float, true>(static_cast<const float*>(logits), R, V, K, sp, c, c64, none, o, st);
-  }
-  o.keys = reinterpret_cast<uint64_t*>(w);
-  o.parts = reinterpret_cast<Mass*>(w + pl.off_parts);
-  hipError_t e;
-  if (dtype == DSPARK_BF16)
-    e = launch_segments<uint16_t, false>(static_cast<const uint16_t*>(logits), R, V, K, sp, c, c64, none, o, st);
-  else
-    e = launch_segments<float, false>(static_cast<const float*>(logits), R, V, K, sp, c, c64, none, o, st);
-  if (e != hipSuccess) return e;
-  return launch_merge<true>(o.keys, o.parts, R, K, sp.P, c, c64, none, o, st);
+  return launch_rows<kRows>(logits, dtype, R, V, K, top_split(epl, R, V, any_alignment(logits, V, epl)), temperature,
+                            TopBeams{}, TopOut{values, ids, rest, lse, flags, nullptr, nullptr},
+                            reinterpret_cast<uint64_t*>(w), reinterpret_cast<Mass*>(w + pl.off_parts), st);
 }
 
-// Beams: rows of live beams, their lists left in the workspace.
-int top_lists_segments(int dtype, int32_t R, int32_t V, int32_t K, const void* logits) {
+hipError_t launch_beam_rows(const void* logits, int dtype, int32_t R, int32_t V, int32_t M, const float* scores,
+                            const uint8_t* finished, int32_t eos, uint64_t* sums, uint64_t* keys, uint8_t* flags,
+                            void* ws, const TopPlan& pl, hipStream_t st) {
   const int epl = dtype == DSPARK_BF16 ? 8 : 4;
-  return top_split(epl, R, V, K, any_alignment(logits, V, epl)).P;
-}
-
-hipError_t launch_top_lists(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, const float* scores,
-                            const uint8_t* finished, uint64_t* keys, Mass* parts, hipStream_t st) {
-  const int epl = dtype == DSPARK_BF16 ? 8 : 4;
-  const TopSplit sp = top_split(epl, R, V, K, any_alignment(logits, V, epl));
-  const TopSkip skip{scores, finished};
-  const TopOut o{nullptr, nullptr, nullptr, nullptr, nullptr, keys, parts};
-  const float c = mass_scale(1.0f);
-  const double c64 = mass_scale64(1.0f);
-  if (dtype == DSPARK_BF16)
-    return launch_segments<uint16_t, false>(static_cast<const uint16_t*>(logits), R, V, K, sp, c, c64, skip, o, st);
-  return launch_segments<float, false>(static_cast<const float*>(logits), R, V, K, sp, c, c64, skip, o, st);
-}
-
-hipError_t launch_top_lists_merge(const uint64_t* keys, const Mass* parts, int32_t R, int32_t K, int32_t P,
-                                  const float* scores, const uint8_t* finished, uint64_t* out_keys, Mass* out_parts,
-                                  hipStream_t st) {
-  const TopOut o{nullptr, nullptr, nullptr, nullptr, nullptr, out_keys, out_parts};
-  return launch_merge<false>(keys, parts, R, K, P, mass_scale(1.0f), mass_scale64(1.0f), TopSkip{scores, finished}, o,
-                             st);
+  char* w = static_cast<char*>(ws);
+  return launch_rows<kBeams>(logits, dtype, R, V, M, top_split(epl, R, V, any_alignment(logits, V, epl)), 1.0f,
+                             TopBeams{scores, finished, eos, sums, flags},
+                             TopOut{nullptr, nullptr, nullptr, nullptr, nullptr, keys, nullptr},
+                             reinterpret_cast<uint64_t*>(w), reinterpret_cast<Mass*>(w + pl.off_parts), st);
 }
 
 }  // namespace dspark

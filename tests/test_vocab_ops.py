@@ -88,9 +88,9 @@ def test_top_logits_refusals(L):
     assert top(L, logits=C.c_void_p(4097)) == ds.DSPARK_EINVAL
     assert top(L, logits=C.c_void_p(4098), dtype=2) == ds.DSPARK_EINVAL
     assert top(L, R=0, logits=None, out=None, ws=None) == ds.DSPARK_OK
-    assert ds.dspark_workspace_size(ds.DSPARK_OP_TOP, 1, 1, 129280, 8) > 0
-    assert top(L, R=1, V=129280, ws=None) == ds.DSPARK_EWORKSPACE
-    assert top(L, R=1, V=129280, wsb=64) == ds.DSPARK_EWORKSPACE
+    assert ds.dspark_workspace_size(ds.DSPARK_OP_TOP, 1, 1, 1000000, 8) > 0
+    assert top(L, R=1, V=1000000, ws=None) == ds.DSPARK_EWORKSPACE
+    assert top(L, R=1, V=1000000, wsb=64) == ds.DSPARK_EWORKSPACE
     assert ds.dspark_workspace_size(ds.DSPARK_OP_TOP, 4, 1, 1024, 0) == 0
     assert ds.dspark_workspace_size(ds.DSPARK_OP_TOP, 4, 1, 1024, ds.DSPARK_MAX_TOP + 1) == 0
 
