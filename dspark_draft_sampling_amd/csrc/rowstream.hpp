@@ -67,6 +67,10 @@ __device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Keeps the compiler from holding a granule's unpacked elements in registers
+// from one pass over them to the next (they are one instruction away).
+__device__ __forceinline__ void repack(uint4& u) { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }
+
 // L granules per thread, q0 + i NT + tid: one branch on the whole group (uniform)
 // keeps the interior loads free of per-lane checks.
 template <typename T, int NT, int L>
@@ -220,13 +224,16 @@ __device__ __forceinline__ double key_double(uint64_t k) {
 template <int NW>
 __device__ __forceinline__ int block_scan(int v, int* slots, int& total) {
   const int lane = threadIdx.x & 63;
+  // within rows of 16 lanes by DPP row shifts (lanes shifted in from outside give
+  // 0), then the last lanes of the rows before
   int inc = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(inc, d, 64);
-    if (lane >= d) inc += up;
-  }
-  const int all = lane_i(inc, 63);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xF, 0xF, true);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xF, 0xF, true);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xF, 0xF, true);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xF, 0xF, true);
+  const int r0 = lane_i(inc, 15), r1 = r0 + lane_i(inc, 31), r2 = r1 + lane_i(inc, 47);
+  const int all = r2 + lane_i(inc, 63);
+  inc += lane < 16 ? 0 : lane < 32 ? r0 : lane < 48 ? r1 : r2;
   if constexpr (NW == 1) {
     total = all;
     return inc - v;

@@ -43,8 +43,8 @@ constexpr int kL = 4;              // granules of a group
 // once: more are first cut by a search.
 template <int NT>
 struct TopCaps {
-  static constexpr int kG = NT == 1024 ? 8 : 16;
-  static constexpr int kRank = NT == 64 ? 128 : NT == 256 ? 512 : 1024;
+  static constexpr int kG = NT == 512 ? 8 : 16;
+  static constexpr int kRank = NT == 64 ? 128 : 512;
 };
 
 // Candidates a list may hold beyond K: the searches stop at the first bound
@@ -198,10 +198,10 @@ __device__ __forceinline__ Mass gran_mass(const uint4& u, int e0, float c, F&& k
     if (!keep(x[j], e0 + j)) x[j] = neg_inf();
     m = fmaxf(m, x[j]);
   }
-  if (m == neg_inf()) return mass_none();
-  float s = 0.0f;
+  const float ref = m > neg_inf() ? m : 0.0f;
+  float s = 0.0f;  // a NaN, too, ends up here
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) s += __builtin_amdgcn_exp2f(mass_gap(x[j], m, c));
+  for (int j = 0; j < EPL; ++j) s += __builtin_amdgcn_exp2f(mass_gap(x[j], ref, c));
   return Mass{m, s};
 }
 
@@ -222,11 +222,11 @@ struct TopLds {
 };
 
 // Candidates of a segment by a search over its elements (rows where the bound
-// lets too many through): exactly K keys into s.cand, returned, and the mass of
-// all other elements as each thread's share.
+// lets too many through): exactly K keys into cand, their number returned, and
+// the mass of all other elements as each thread's share.  scan: NW ints.
 template <typename T, int NT>
 __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1, int K, uint32_t kmax, float c,
-                                                TopLds<NT>& s, int& step, Mass& others) {
+                                                uint64_t* cand, int* slots, int* scan, int& step, Mass& others) {
   constexpr int NW = NT / 64;
   constexpr int EPL = Row<T>::EPL;
   const int tid = threadIdx.x;
@@ -248,7 +248,7 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
         n.c += k >= t3;
       }
     }
-    return block_count<NW>(Count3{wave_total(n.a), wave_total(n.b), wave_total(n.c)}, s.slots, step);
+    return block_count<NW>(Count3{wave_total(n.a), wave_total(n.b), wave_total(n.c)}, slots, step);
   });
   // of the elements at t the lowest indices: the least `last` with K keys above t or at t up to it
   int32_t last = r.V - 1;
@@ -266,7 +266,7 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
         }
       }
       n.a = wave_total(n.a);
-      if (block_count<NW>(n, s.slots, step).a >= K) {
+      if (block_count<NW>(n, slots, step).a >= K) {
         last = mid;
       } else {
         lo = mid;
@@ -285,7 +285,7 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
     }), c);
   }
   int total;
-  int pos = block_scan<NW>(mine, s.scan[0], total);
+  int pos = block_scan<NW>(mine, scan, total);
   __syncthreads();
   for (int q = q0 + tid; q < q1; q += NT) {
     const uint4 u = gran_load(r, q);
@@ -293,7 +293,7 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
     for (int j = 0; j < EPL; ++j) {
       const float x = gran_elem(u, j, T{});
       const uint64_t k = cand_key(order_key(x), q * EPL - r.head + j);
-      if (k >= kth && x > neg_inf()) s.cand[pos++] = k;
+      if (k >= kth && x > neg_inf()) cand[pos++] = k;
     }
   }
   __syncthreads();
@@ -430,30 +430,33 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
           return first + (g / NT * kL + i % kL) * NT + g % NT;
         };
         mine = 0;
+        uint4 mineu = make_uint4(0, 0, 0, 0);  // the thread's first granule
         for (int i = tid; i < nq * kL; i += NT) {
           const int q = granule(i);
           if (q >= q1) continue;
-          others = mass_add(others, gran_mass<T>(gran_load(r, q), 0, c, [&](float x, int) {
+          const uint4 u = gran_load(r, q);
+          if (i == tid) mineu = u;
+          others = mass_add(others, gran_mass<T>(u, 0, c, [&](float x, int) {
             mine += x >= at;
             return !(x >= at);
           }), c);
         }
         pos = block_scan<NW>(mine, s.scan[1], nc);
-        if (nc <= CAND) {
+        if (nc <= CAND && mine > 0) {
           for (int i = tid; i < nq * kL; i += NT) {
             const int q = granule(i);
             if (q >= q1) continue;
-            const uint4 u = gran_load(r, q);
+            const uint4 u = i == tid ? mineu : gran_load(r, q);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
               const float x = gran_elem(u, j, T{});
               if (x >= at) s.cand[pos++] = cand_key(order_key(x), q * EPL - r.head + j);
             }
           }
-          __syncthreads();
         }
+        __syncthreads();
       }
-      if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s, step, others);
+      if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s.cand, s.slots, s.scan[0], step, others);
 
       // ---- the K best of them or a few more; the others' mass ----
       nl = nc;
@@ -505,6 +508,139 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
       if (tid == 0) o.parts[row * P + seg] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
     }
     __syncthreads();  // LDS is reused by the next item
+  }
+}
+
+// Short rows: one wave a row, the row in registers (L granules a lane).  The
+// bound comes from the granules' maxima; candidates leave the registers, and one
+// pass of exponentials over what stays gives the others' mass.  Nothing is read
+// twice.
+constexpr int kSmallCand = 448;
+
+template <typename T, int L, TopMode MODE>
+__global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ logits, int32_t R, int32_t V, int32_t K,
+                                                       float c, double c64, TopBeams bm, TopOut o) {
+  constexpr int EPL = Row<T>::EPL;
+  __shared__ uint64_t cand[kSmallCand + 4];
+  __shared__ uint64_t sorted[kMaxList];
+  const int lane = threadIdx.x;
+  int step = 0;
+  for (int row = blockIdx.x; row < R; row += gridDim.x) {
+    const size_t at_row = static_cast<size_t>(row);
+    if (unread_beam<64, MODE>(bm, o, at_row, K)) continue;
+    const Row<T> r = make_row(logits + at_row * V, V);
+    uint4 u[L];
+    group_load<T, 64, L>(r, 0, lane, u);
+    float gm[L], lmax = neg_inf();
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      gm[i] = neg_inf();
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) gm[i] = fmaxf(gm[i], gran_elem(u[i], j, T{}));
+      lmax = fmaxf(lmax, gm[i]);
+    }
+    const float wmax = wave_max(lmax);
+    bool bad = wmax == pos_inf(), slow = false;
+    Mass others = mass_none();
+    uint64_t* list = cand;
+    int nl = 0;  // candidates listed
+    if (!bad && wmax > neg_inf()) {
+      // ---- bound: at least K granules (or all finite ones) reach it ----
+      const uint32_t kmax = order_key(wmax);
+      const float wmin = -wave_max(-lmax);
+      auto granules_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+        Count3 n{0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const uint32_t k = order_key(gm[i]);
+          n.a += __popcll(__ballot(k >= t1));
+          n.b += __popcll(__ballot(k >= t2));
+          n.c += __popcll(__ballot(k >= t3));
+        }
+        return n;
+      };
+      uint32_t bound = K <= 64 && wmin > neg_inf() ? order_key(wmin) : kKeyNegInf + 1;
+      int nb = granules_at(bound, bound, bound).a;
+      if (nb > K) bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), granules_at);
+      // ---- the elements that reach it leave the registers ----
+      const float at = key_value(bound);
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        repack(u[i]);
+        if (__any(gm[i] >= at)) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) mine += gran_elem(u[i], j, T{}) >= at;
+        }
+      }
+      int pos = block_scan<1>(mine, nullptr, nl);
+      slow = nl > kSmallCand;
+      if (slow) {
+        nl = exact_candidates<T, 64>(r, 0, r.Q, K, kmax, c, cand, nullptr, nullptr, step, others);
+      } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          repack(u[i]);
+          if (__any(gm[i] >= at)) {
+            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+              const float x = gran_elem(u[i], j, T{});
+              if (x >= at) {
+                cand[pos++] = cand_key(order_key(x), (i * 64 + lane) * EPL - r.head + j);
+                if constexpr (sizeof(T) == 2)
+                  w[j / 2] = (j & 1) ? (w[j / 2] & 0x0000ffffu) | 0xFF800000u : (w[j / 2] & 0xffff0000u) | 0xFF80u;
+                else
+                  w[j] = 0xFF800000u;
+              }
+            }
+            u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncthreads();
+        if (MODE == kBeams && nl > list_len(K)) {
+          const uint64_t t = list_bound<64>(cand, nl, nl, K, static_cast<uint64_t>(bound) << 32,
+                                            static_cast<uint64_t>(kmax + 1) << 32, nullptr, step);
+          mine = 0;
+          for (int i = lane; i < nl; i += 64) mine += cand[i] >= t;
+          int n;
+          pos = block_scan<1>(mine, nullptr, n);
+          for (int i = lane; i < nl; i += 64) {
+            const uint64_t k = cand[i];
+            if (k >= t) {
+              sorted[pos++] = k;
+            } else {
+              others = mass_add(others, Mass{key_value(k), 1.0f}, c);
+            }
+          }
+          __syncthreads();
+          list = sorted;
+          nl = n;
+        }
+      }
+    }
+    if (!slow) {
+#pragma unroll
+      for (int i = 0; i < L; i += 4) {
+        uint4 v[4] = {u[i], u[i + 1], u[i + 2], u[i + 3]};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) repack(v[k]);
+        others = mass_add(others, group_mass<T, 4>(v, c), c);
+      }
+    }
+    if constexpr (MODE == kRows) {
+      rank_keys<64>(cand, nl, K, sorted);
+      const uint64_t kth = sorted[K - 1];
+      for (int i = lane; i < nl; i += 64)
+        if (cand[i] < kth) others = mass_add(others, Mass{key_value(cand[i]), 1.0f}, c);
+    }
+    others = wave_mass(others, c);
+    bad |= !(others.s >= 0.0f);
+    if constexpr (MODE == kRows)
+      write_row(o, at_row, sorted, K, others, bad, c, c64);
+    else
+      write_beam(bm, o, at_row, list, nl, K, others, bad, c, c64);
+    __syncthreads();  // LDS is reused by the next row
   }
 }
 
@@ -594,23 +730,27 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
   }
 }
 
-// Rows are cut into segments of `groups` groups a thread.  Many short rows are
-// taken by a wave each; many rows by workgroups of 256 threads, of which several
-// share a compute unit; few rows by workgroups of 1024.
-TopSplit top_split(int epl, int64_t R, int32_t V, bool any) {
+// Rows are cut into segments of `groups` groups a thread; groups = 0: short rows,
+// NT granules a lane of one wave.
+TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
   // granules of a row, at the least favourable alignment
   const int q = any ? (V + 2 * epl - 2) / epl : V / epl;
   TopSplit s{};
+  s.P = 1;
+  if (q <= 8 * 64) {
+    s.NT = q <= 4 * 64 ? 4 : 8;
+    return s;
+  }
   int most;
-  if (q <= 2 * 64 * kL || (q <= TopCaps<64>::kG * 64 * kL && R >= 4096)) {
+  if (q <= TopCaps<64>::kG * 64 * kL && R >= 2048 && K <= 32) {
     s.NT = 64;
     most = TopCaps<64>::kG;
-  } else if (q <= 2 * 256 * kL || R >= 1024) {
+  } else if (q > 4 * 256 * kL && R <= 512) {
+    s.NT = 512;
+    most = TopCaps<512>::kG;
+  } else {
     s.NT = 256;
     most = TopCaps<256>::kG;
-  } else {
-    s.NT = 1024;
-    most = TopCaps<1024>::kG;
   }
   const int need = (q + s.NT * kL - 1) / (s.NT * kL);  // groups of a thread over the row
   s.P = (need + most - 1) / most;
@@ -631,8 +771,22 @@ hipError_t launch_segments(const T* logits, int32_t R, int32_t V, int32_t K, con
   else if (sp.NT == 256)
     DSPARK_TOP(256);
   else
-    DSPARK_TOP(1024);
+    DSPARK_TOP(512);
 #undef DSPARK_TOP
+  return hipGetLastError();
+}
+
+template <typename T, TopMode MODE>
+hipError_t launch_small(const T* logits, int32_t R, int32_t V, int32_t K, const TopSplit& sp, float c, double c64,
+                        const TopBeams& bm, const TopOut& o, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(std::min(R, kMaxGrid)));
+#define DSPARK_SMALL(L)                                                                                             \
+  DSPARK_LAUNCH("top_small", (top_small_kernel<T, L, MODE>), grid, dim3(64), 0, st, logits, R, V, K, c, c64, bm, o)
+  if (sp.NT == 4)
+    DSPARK_SMALL(4);
+  else
+    DSPARK_SMALL(8);
+#undef DSPARK_SMALL
   return hipGetLastError();
 }
 
@@ -644,6 +798,9 @@ hipError_t launch_rows(const void* logits, int dtype, int32_t R, int32_t V, int3
   const double c64 = mass_scale64(temperature);
   const uint16_t* h = static_cast<const uint16_t*>(logits);
   const float* f = static_cast<const float*>(logits);
+  if (sp.groups == 0)
+    return dtype == DSPARK_BF16 ? launch_small<uint16_t, MODE>(h, R, V, K, sp, c, c64, bm, o, st)
+                                : launch_small<float, MODE>(f, R, V, K, sp, c, c64, bm, o, st);
   if (sp.P == 1)
     return dtype == DSPARK_BF16 ? launch_segments<uint16_t, MODE>(h, R, V, K, sp, c, c64, bm, o, st)
                                 : launch_segments<float, MODE>(f, R, V, K, sp, c, c64, bm, o, st);
@@ -675,7 +832,7 @@ TopPlan plan_top(int32_t R, int32_t V, int32_t K) {
   int P = 1;
   for (const int epl : {4, 8})
     for (const bool any : {false, true})
-      if (any || V % epl == 0) P = std::max(P, top_split(epl, R, V, any).P);
+      if (any || V % epl == 0) P = std::max(P, top_split(epl, R, V, K, any).P);
   p.P = P;
   const size_t rp = static_cast<size_t>(R) * P;
   size_t off = 0;
@@ -693,7 +850,7 @@ hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32
                       hipStream_t st) {
   const int epl = dtype == DSPARK_BF16 ? 8 : 4;
   char* w = static_cast<char*>(ws);
-  return launch_rows<kRows>(logits, dtype, R, V, K, top_split(epl, R, V, any_alignment(logits, V, epl)), temperature,
+  return launch_rows<kRows>(logits, dtype, R, V, K, top_split(epl, R, V, K, any_alignment(logits, V, epl)), temperature,
                             TopBeams{}, TopOut{values, ids, rest, lse, flags, nullptr, nullptr},
                             reinterpret_cast<uint64_t*>(w), reinterpret_cast<Mass*>(w + pl.off_parts), st);
 }
@@ -703,7 +860,7 @@ hipError_t launch_beam_rows(const void* logits, int dtype, int32_t R, int32_t V,
                             void* ws, const TopPlan& pl, hipStream_t st) {
   const int epl = dtype == DSPARK_BF16 ? 8 : 4;
   char* w = static_cast<char*>(ws);
-  return launch_rows<kBeams>(logits, dtype, R, V, M, top_split(epl, R, V, any_alignment(logits, V, epl)), 1.0f,
+  return launch_rows<kBeams>(logits, dtype, R, V, M, top_split(epl, R, V, M, any_alignment(logits, V, epl)), 1.0f,
                              TopBeams{scores, finished, eos, sums, flags},
                              TopOut{nullptr, nullptr, nullptr, nullptr, nullptr, keys, nullptr},
                              reinterpret_cast<uint64_t*>(w), reinterpret_cast<Mass*>(w + pl.off_parts), st);
