@@ -121,7 +121,7 @@ size_t dspark_workspace_size(int op, int32_t B, int32_t gamma, int32_t V, int32_
     case DSPARK_OP_TOP:
       return r <= 0 || r > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB ? 0 : dspark::plan_top(B, V, r).bytes;
     case DSPARK_OP_DISTILL:
-      return dspark::plan_distill(B, gamma, V).bytes;
+      return dspark::distill_bytes();
     case DSPARK_OP_BEAM:
       return r <= 0 || r > DSPARK_MAX_TOP || V > DSPARK_MAX_TOP_VOCAB || gamma > DSPARK_MAX_BEAMS ||
                      static_cast<int64_t>(B) * gamma > 0x7fffffffLL
@@ -334,11 +334,10 @@ dspark_status dspark_distill(const void* draft_logits, int logits_dtype, const f
   if (N > 0 && (!draft_logits || !teacher_values || !teacher_ids || !kl || !lse || !rest || !flags ||
                 !aligned_to(draft_logits, logits_dtype)))
     return DSPARK_EINVAL;
-  const dspark::DistillPlan plan = dspark::plan_distill(N, gamma, V);
-  if (N > 0 && (!workspace || workspace_bytes < plan.bytes)) return DSPARK_EWORKSPACE;
+  if (N > 0 && (!workspace || workspace_bytes < dspark::distill_bytes())) return DSPARK_EWORKSPACE;
   const hipError_t e = dspark::launch_distill(draft_logits, logits_dtype, teacher_values, teacher_ids, teacher_rest,
                                               block_mask, N, gamma, V, K, temperature, weight, kl, lse, rest, flags,
-                                              sums, workspace, plan, static_cast<hipStream_t>(stream));
+                                              sums, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? DSPARK_OK : DSPARK_EDEVICE;
 }
 

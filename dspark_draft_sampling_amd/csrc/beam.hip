@@ -6,8 +6,8 @@
 //
 // Selection: a beam's M best tokens hold all that the request can take from
 // it, so the rows go through the pass of top.hip (one read of each live beam's
-// row; ended and dead beams are not read), which leaves per beam a list with its
-// M best candidates and their scores in 64 bits: candidates of two beams can
+// row; ended and dead beams are not read), which leaves per beam its M best
+// candidates in order with their scores in 64 bits: candidates of two beams can
 // stand closer than 32 bits tell apart.  beam_final, one workgroup a request,
 // ranks them: a candidate's rank is the number of better ones; of many, a search
 // over the scores' order keys keeps M or a few more first.  Equal scores go by
@@ -27,13 +27,13 @@ namespace {
 
 constexpr int kFinalThreads = 256;
 constexpr int kFinalWaves = kFinalThreads / 64;
-constexpr int kMaxCand = 5376;  // DSPARK_MAX_BEAMS lists of the longest length
+constexpr int kMaxCand = DSPARK_MAX_BEAMS * DSPARK_MAX_TOP;
 constexpr int kRankAll = 128;   // candidates ranked at once; more are first cut by a search
 constexpr int kMaxGrid = 1 << 20;
 
 __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ sums,
                                                                    const uint64_t* __restrict__ keys, int32_t B,
-                                                                   int32_t W, int32_t M, int32_t E,
+                                                                   int32_t W, int32_t M,
                                                                    int32_t* __restrict__ tokens,
                                                                    int32_t* __restrict__ parents,
                                                                    float* __restrict__ scores) {
@@ -45,7 +45,8 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
   __shared__ int scan[2][NW];
   __shared__ uint64_t red[2][NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  const int n = W * E;
+  const int n = W * M;
+  const int each = (n + NT - 1) / NT;  // a thread's stretch, so that positions keep their order
   int step = 0;
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
     const uint64_t* key = keys + static_cast<size_t>(b) * n;
@@ -93,37 +94,33 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
     // ---- those that can be among the M ----
     int nb;
     mine = 0;
-    for (int i = tid; i < n; i += NT) mine += sh_sum[i] >= bound;
+    const int i0 = tid * each, i1 = min(n, i0 + each);
+    for (int i = i0; i < i1; ++i) mine += sh_sum[i] >= bound;
     int pos = block_scan<NW>(mine, scan[1], nb);
-    for (int i = tid; i < n; i += NT)
+    for (int i = i0; i < i1; ++i)
       if (sh_sum[i] >= bound) {
         sh_best[pos] = sh_sum[i];
         sh_from[pos++] = static_cast<uint16_t>(i);
       }
     if (tid < 4) sh_best[nb + tid] = 0;
     __syncthreads();
-    // ---- rank: score, then beam, logit, token ----
+    // ---- rank: score, then position, which is beam, logit, token ----
     for (int i = tid; i < nb; i += NT) {
       const uint64_t d = sh_best[i];
-      int rank = 0, same = 0;
+      int rank = 0;
       for (int j = 0; j < nb; j += 4) {
         const uint64_t d0 = sh_best[j], d1 = sh_best[j + 1], d2 = sh_best[j + 2], d3 = sh_best[j + 3];
-        rank += (d0 > d) + (d1 > d) + (d2 > d) + (d3 > d);
-        same += (d0 == d) + (d1 == d) + (d2 == d) + (d3 == d);
+        rank += d0 > d - (j < i) ? 1 : 0;
+        rank += d1 > d - (j + 1 < i) ? 1 : 0;
+        rank += d2 > d - (j + 2 < i) ? 1 : 0;
+        rank += d3 > d - (j + 3 < i) ? 1 : 0;
       }
-      if (rank >= M) continue;
-      const int from = sh_from[i], w = from / E;
-      const uint64_t k = key[from];
-      if (same > 1)
-        for (int j = 0; j < nb; ++j)
-          if (j != i && sh_best[j] == d) {
-            const int wj = sh_from[j] / E;
-            rank += wj < w || (wj == w && key[sh_from[j]] > k);
-          }
       if (rank < M) {
+        const int from = sh_from[i];
+        const uint64_t k = key[from];
         const size_t o = static_cast<size_t>(b) * M + rank;
         tokens[o] = key_index(k);
-        parents[o] = w;
+        parents[o] = from / M;
         scores[o] = static_cast<float>(key_double(d));
       }
     }
@@ -213,7 +210,7 @@ BeamPlan plan_beam(int32_t B, int32_t W, int32_t V, int32_t M) {
   BeamPlan p{};
   const int32_t R = B * W;
   p.rows = plan_top(R, V, M);
-  const size_t list = static_cast<size_t>(R) * top_list_len(M) * sizeof(uint64_t);
+  const size_t list = static_cast<size_t>(R) * M * sizeof(uint64_t);
   size_t off = 0;
   p.off_sums = off;
   off = align_up(off + list, 256);
@@ -234,7 +231,7 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
                                         w + pl.off_rows, pl.rows, st);
   if (e != hipSuccess) return e;
   DSPARK_LAUNCH("beam_final", beam_final_kernel, dim3(static_cast<unsigned>(std::min(B, kMaxGrid))),
-                dim3(kFinalThreads), 0, st, sums, keys, B, W, M, top_list_len(M), tokens, parents, out_scores);
+                dim3(kFinalThreads), 0, st, sums, keys, B, W, M, tokens, parents, out_scores);
   return hipGetLastError();
 }
 

@@ -5,15 +5,17 @@
 // else as one more; kl = sum_j t_j (log t_j - log s_j) over them, with t the
 // teacher's and s the draft's probabilities at temperature T.
 //
-// Loss, two launches.  distill_mass streams the draft rows once and sums the
-// mass of the tokens outside the teacher's list, and of nothing else: the
-// list becomes a bit mask in LDS, one word per thread and group of 4
-// granules, so a group without a listed token (nearly all) costs one LDS read
-// and a branch.  distill_rows, one wave a row, forms the K + 1 outcomes in 64
-// bits from that mass, the teacher's values and the draft's logits at its
-// tokens: where one probability is nearly 1, its logarithm and its difference
-// from the other side keep their accuracy, as no 32-bit normaliser of the
-// whole row enters.
+// Loss: a workgroup streams a draft row once and sums the mass of the tokens
+// outside the teacher's list, and of nothing else: the list becomes a bit mask in
+// LDS, one word per thread and group of 32 logits, so a group without a listed
+// token (nearly all) costs one LDS read and a branch.  Its first wave then forms
+// the K + 1 outcomes in 64 bits from that mass, the teacher's values and the
+// draft's logits at its tokens: where one probability is nearly 1, its logarithm
+// and its difference from the other side keep their accuracy, as no 32-bit
+// normaliser of the whole row enters.  That costs one wave a few hundred 64-bit
+// operations while the compute unit's other workgroups stream.  A second, small
+// launch adds up the sums; a batch of a few short rows is one launch of one
+// workgroup, a wave a row.
 //
 // Gradient, one launch: with d_v the derivative of kl by x_v / T,
 //   v in the list:  d_v = s_v - sum_{j: id_j = v} t_j
@@ -30,13 +32,37 @@ namespace dspark {
 namespace {
 
 constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch; each then takes several items
-constexpr int kL = 4;              // granules per thread and group
-constexpr int kMaxTiles = 16;      // groups per segment
-constexpr int kRowsThreads = 1024; // distill_rows: one wave a row
-constexpr int kRowsWaves = kRowsThreads / 64;
-constexpr int kRowsGrid = 256;
+constexpr int kMaxTiles = 16;      // groups of a thread whose mask words are held at a time
+constexpr int kTinyThreads = 1024; // one-launch form: a wave a row
+constexpr int kTinyWaves = kTinyThreads / 64;
+constexpr int kTinyTiles = 4;
+constexpr int kSumThreads = 1024;
+constexpr int kMaxSumBlocks = 64;
 constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kLog2ed = 1.4426950408889634074;
+
+struct DistillArgs {
+  const float* values;
+  const int32_t* ids;
+  const float* teacher_rest;  // or NULL
+  const uint8_t* block_mask;  // or NULL
+  int32_t N, gamma, V, K;
+  float c;
+  double c64;
+  float weight;
+};
+
+// Barrier of the NT threads that share a row (one wave needs its LDS traffic
+// ordered, no barrier).
+template <int NT>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (NT == 64) {
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
 
 // L granules with -inf at the elements whose bit is set.
 template <typename T, int L>
@@ -58,142 +84,112 @@ __device__ __forceinline__ void mask_out(uint4 (&u)[L], uint32_t word) {
   }
 }
 
-template <typename T, int NT>
-__global__ __launch_bounds__(NT) void distill_mass_kernel(const T* __restrict__ draft, const int32_t* __restrict__ ids,
-                                                          int64_t items, int32_t V, int32_t K, int32_t P, int32_t tiles,
-                                                          float c, Mass* __restrict__ parts,
-                                                          uint32_t* __restrict__ ticket) {
-  constexpr int NW = NT / 64;
-  constexpr int EPL = Row<T>::EPL;
-  __shared__ uint32_t member[kMaxTiles * NT];
-  __shared__ Mass shm[NW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  if (blockIdx.x == 0 && tid == 0) *ticket = 0u;  // of distill_rows
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const size_t row = static_cast<size_t>(item / P);
-    const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
-    const Row<T> r = make_row(draft + row * V, V);
-    const int first = seg * tiles * (NT * kL);
-    const int n = min(tiles, (r.Q - first + NT * kL - 1) / (NT * kL));  // groups; <= 0: none
-    uint4 a[kL], b[kL];
-    if (n > 0) group_load<T, NT, kL>(r, first, tid, a);
-    for (int g = 0; g < n; ++g) member[g * NT + tid] = 0u;
-    __syncthreads();
-    for (int j = tid; j < K; j += NT) {
-      const int32_t id = ids[row * K + j];
-      if (id >= 0 && id < V) {
-        const int e = id + r.head, q = e / EPL - first;
-        if (q >= 0 && q < n * NT * kL) {
-          const int g = q / (NT * kL), i = (q / NT) % kL;
-          atomicOr(&member[g * NT + q % NT], 1u << (i * EPL + e % EPL));
-        }
-      }
-    }
-    __syncthreads();
-    Mass acc = mass_none();
-    auto take = [&](uint4(&u)[kL], int g) {
-      const uint32_t word = member[g * NT + tid];
-      if (__any(word != 0)) mask_out<T, kL>(u, word);
-      acc = mass_add(acc, group_mass<T, kL>(u, c), c);
-    };
-    for (int g = 0; g < n; g += 2) {
-      if (g + 1 < n) group_load<T, NT, kL>(r, first + (g + 1) * NT * kL, tid, b);
-      take(a, g);
-      if (g + 1 >= n) break;
-      if (g + 2 < n) group_load<T, NT, kL>(r, first + (g + 2) * NT * kL, tid, a);
-      take(b, g + 1);
-    }
-    acc = wave_mass(acc, c);
-    if constexpr (NW > 1) {
-      if (lane == 0) shm[wave] = acc;
-      __syncthreads();
-      if (wave == 0) acc = wave_mass(lane < NW ? shm[lane] : mass_none(), c);
-    }
-    if (tid == 0) parts[item] = acc;
-    __syncthreads();  // LDS is reused by the next item
-  }
-}
-
 // ---- the K + 1 outcomes of a row, by one wave --------------------------------------
-// Lane l holds entries l and l + 64.  Everything in base-2 logarithms and 64 bits.
-constexpr int kEnt = DSPARK_MAX_TOP / 64;
-
-struct Outcomes {
-  double lt[kEnt];     // log2 t_j (-inf: no such entry)
-  double ls[kEnt];     // log2 s at its token
-  int32_t id[kEnt];    // its token, -1: none
-  bool first[kEnt];    // no earlier entry of the row has the same token
-  double lt_r, ls_r;   // everything else
-  double lse;          // log2 of the draft's whole mass
-  bool bad;            // a NaN or +inf
-  bool empty;          // no mass on one side
+// Lane l holds entries l, l + 64, ..  ENT: entries of a lane (K <= 64 ENT).
+template <int ENT>
+struct Entries {
+  int32_t id[ENT];  // its token, -1: none
+  float v[ENT];     // the teacher's logit
+  float x[ENT];     // the draft's
+  float trest;      // the teacher's other mass
 };
 
-template <typename T>
-__device__ __forceinline__ Outcomes outcomes(const Row<T>& r, const float* __restrict__ values,
-                                             const int32_t* __restrict__ ids, const float* __restrict__ teacher_rest,
-                                             size_t row, int K, double rest2, double c64, int32_t* sh_ids) {
+template <typename T, int ENT>
+__device__ __forceinline__ Entries<ENT> load_entries(const Row<T>& r, const DistillArgs& a, size_t row) {
   const int lane = threadIdx.x & 63;
-  Outcomes o;
-  double zt[kEnt], zs[kEnt];
-  bool bad = isnan(rest2) || rest2 == __builtin_inf();
-  double zr = -__builtin_inf();
-  if (teacher_rest) {
-    const float t = teacher_rest[row];
-    bad |= !(t < pos_inf());
-    zr = static_cast<double>(t) * kLog2ed;
-  }
-  double mt = zr, ms = rest2;
+  Entries<ENT> e;
+  e.trest = a.teacher_rest ? a.teacher_rest[row] : neg_inf();
 #pragma unroll
-  for (int i = 0; i < kEnt; ++i) {
+  for (int i = 0; i < ENT; ++i) {
     const int j = i * 64 + lane;
-    o.id[i] = -1;
-    zt[i] = zs[i] = -__builtin_inf();
-    if (j < K) {
-      const int32_t id = ids[row * K + j];
+    e.id[i] = -1;
+    e.v[i] = e.x[i] = neg_inf();
+    if (j < a.K) {
+      const int32_t id = a.ids[row * a.K + j];
+      const float v = a.values[row * a.K + j];
       if (id >= 0 && id < r.V) {
-        o.id[i] = id;
-        const float v = values[row * K + j], x = load_logit(r.p, static_cast<size_t>(id));
-        bad |= !(v < pos_inf()) || !(x < pos_inf());
-        zt[i] = static_cast<double>(v) * c64;
-        zs[i] = static_cast<double>(x) * c64;
+        e.id[i] = id;
+        e.v[i] = v;
+        e.x[i] = load_logit(r.p, static_cast<size_t>(id));
       }
     }
-    sh_ids[j] = o.id[i];
-    mt = fmax(mt, zt[i]);
-    ms = fmax(ms, zs[i]);
   }
-  __builtin_amdgcn_wave_barrier();
-  __threadfence_block();
-  // an earlier entry with the same token
+  return e;
+}
+
+// Everything in base-2 logarithms and 64 bits.
+template <int ENT>
+struct Outcomes {
+  double lt[ENT];   // log2 t_j (-inf: no such entry)
+  double ls[ENT];   // log2 s at its token
+  double lt_r, ls_r;  // everything else
+  double lse;       // log2 of the draft's whole mass
+  uint32_t first;   // bit i: no earlier entry of the row has entry i's token
+  bool twice;       // some token is listed more than once
+  bool bad;         // a NaN or +inf
+  bool empty;       // no mass on one side
+};
+
+template <int ENT>
+__device__ __forceinline__ Outcomes<ENT> outcomes(const Entries<ENT>& e, int K, double rest2, double c64,
+                                                  int32_t* sh_ids) {
+#pragma clang fp contract(off)  // a value less itself as the reference is 0
+  const int lane = threadIdx.x & 63;
+  Outcomes<ENT> o;
+  bool bad = isnan(rest2) || rest2 == __builtin_inf() || !(e.trest < pos_inf());
+  // the largest values, as references (in 32 bits: they only set the scale)
+  const double zr = static_cast<double>(e.trest) * kLog2ed;
+  float mt = neg_inf(), ms = neg_inf();
 #pragma unroll
-  for (int i = 0; i < kEnt; ++i) o.first[i] = o.id[i] >= 0;
-  for (int j = 0; j < K; ++j) {
-    const int32_t id = sh_ids[j];
-#pragma unroll
-    for (int i = 0; i < kEnt; ++i) o.first[i] = o.first[i] && !(id == o.id[i] && j < i * 64 + lane);
+  for (int i = 0; i < ENT; ++i) {
+    sh_ids[i * 64 + lane] = e.id[i];
+    bad |= e.id[i] >= 0 && (!(e.v[i] < pos_inf()) || !(e.x[i] < pos_inf()));
+    mt = fmaxf(mt, e.v[i]);
+    ms = fmaxf(ms, e.x[i]);
   }
+  row_sync<64>();
+  // entries of the same token
+  int same[ENT] = {};
+  for (int j = 0; j < K; j += 4) {
+    const int4 d = *reinterpret_cast<const int4*>(sh_ids + j);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    mt = fmax(mt, __shfl_xor(mt, d, 64));
-    ms = fmax(ms, __shfl_xor(ms, d, 64));
+    for (int i = 0; i < ENT; ++i)
+      same[i] += (d.x == e.id[i]) + (d.y == e.id[i]) + (d.z == e.id[i]) + (d.w == e.id[i]);
   }
-  double st = 0.0, ss = 0.0;
-  const double nt = mt == -__builtin_inf() ? 0.0 : mt, ns = ms == -__builtin_inf() ? 0.0 : ms;
+  o.first = 0;
+  bool twice = false;
 #pragma unroll
-  for (int i = 0; i < kEnt; ++i) {
-    if (i * 64 >= K) break;
-    st += exp2(zt[i] - nt);
-    if (o.first[i]) ss += exp2(zs[i] - ns);
+  for (int i = 0; i < ENT; ++i) {
+    o.first |= e.id[i] >= 0 ? 1u << i : 0u;
+    twice |= e.id[i] >= 0 && same[i] > 1;
   }
-  st = wave_sum64(st) + exp2(zr - nt);
-  ss = wave_sum64(ss) + exp2(rest2 - ns);
+  o.twice = __any(twice);
+  if (o.twice)
+    for (int j = 0; j < K; ++j) {
+      const int32_t id = sh_ids[j];
+#pragma unroll
+      for (int i = 0; i < ENT; ++i)
+        if (id == e.id[i] && j < i * 64 + lane) o.first &= ~(1u << i);
+    }
+  const double nt = fmax(static_cast<double>(wave_max(mt)) * c64, zr);
+  const double ns = fmax(static_cast<double>(wave_max(ms)) * c64, rest2);
+  const double rt = nt == -__builtin_inf() ? 0.0 : nt, rs = ns == -__builtin_inf() ? 0.0 : ns;
+  double st = 0.0, ss = 0.0, zt[ENT], zs[ENT];
+#pragma unroll
+  for (int i = 0; i < ENT; ++i) {
+    zt[i] = static_cast<double>(e.v[i]) * c64;
+    zs[i] = static_cast<double>(e.x[i]) * c64;
+    st += exp2(zt[i] - rt);
+    if ((o.first >> i) & 1u) ss += exp2(zs[i] - rs);
+  }
+  st = wave_sum64(st) + exp2(zr - rt);
+  ss = wave_sum64(ss) + exp2(rest2 - rs);
   o.bad = __any(bad);
   o.empty = !(st > 0.0) || !(ss > 0.0);
-  const double lt = nt + log2(st);
-  o.lse = ns + log2(ss);
+  const double lt = rt + log2(st);
+  o.lse = rs + log2(ss);
 #pragma unroll
-  for (int i = 0; i < kEnt; ++i) {
+  for (int i = 0; i < ENT; ++i) {
     o.lt[i] = zt[i] - lt;
     o.ls[i] = zs[i] - o.lse;
   }
@@ -202,106 +198,199 @@ __device__ __forceinline__ Outcomes outcomes(const Row<T>& r, const float* __res
   return o;
 }
 
-struct DistillArgs {
-  const float* values;
-  const int32_t* ids;
-  const float* teacher_rest;  // or NULL
-  const uint8_t* block_mask;  // or NULL
-  int32_t N, gamma, V, K, P;
-  float c;
-  double c64;
-  float weight;
+// ---- loss ---------------------------------------------------------------------------
+
+// Log2 of the draft's mass outside the list, by the NT threads of a row; valid
+// on the first wave.  member: TILES NT words; shm: one Mass a wave.
+template <typename T, int NT, int TILES>
+__device__ __forceinline__ double outside_mass(const Row<T>& r, const DistillArgs& a, size_t row, int tid,
+                                               uint32_t* member, Mass* shm) {
+  constexpr int EPL = Row<T>::EPL, L = group_granules<T>(), TILE = NT * L;
+  const int groups = (r.Q + TILE - 1) / TILE;
+  Mass acc = mass_none();
+  uint4 u[L], w[L];
+  group_load<T, NT, L>(r, 0, tid, u);
+  for (int g0 = 0; g0 < groups; g0 += TILES) {
+    const int n = min(TILES, groups - g0);
+    for (int g = 0; g < n; ++g) member[g * NT + tid] = 0u;
+    row_sync<NT>();
+    for (int j = tid; j < a.K; j += NT) {
+      const int32_t id = a.ids[row * a.K + j];
+      if (id >= 0 && id < r.V) {
+        const int e = id + r.head, q = e / EPL - g0 * TILE;
+        if (q >= 0 && q < n * TILE)
+          atomicOr(&member[q / TILE * NT + q % NT], 1u << (q / NT % L * EPL + e % EPL));
+      }
+    }
+    row_sync<NT>();
+    auto take = [&](uint4(&v)[L], int g) {
+      const uint32_t word = member[g * NT + tid];
+      if (__any(word != 0)) mask_out<T, L>(v, word);
+      acc = mass_add(acc, group_mass<T, L>(v, a.c), a.c);
+    };
+    for (int g = 0; g < n; g += 2) {
+      if (g0 + g + 1 < groups) group_load<T, NT, L>(r, (g0 + g + 1) * TILE, tid, w);
+      take(u, g);
+      if (g + 1 >= n) break;  // n is even where more groups follow
+      if (g0 + g + 2 < groups) group_load<T, NT, L>(r, (g0 + g + 2) * TILE, tid, u);
+      take(w, g + 1);
+    }
+    row_sync<NT>();
+  }
+  acc = wave_mass(acc, a.c);
+  if constexpr (NT > 64) {
+    const int lane = tid & 63, wave = wave_id();
+    if (lane == 0) shm[wave] = acc;
+    __syncthreads();
+    if (wave == 0) acc = wave_mass(lane < NT / 64 ? shm[lane] : mass_none(), a.c);
+  }
+  return mass_log2(acc, a.c, a.c64);
+}
+
+struct LossOut {
+  float* kl;
+  float* lse;
+  float* rest;
+  uint8_t* flags;
 };
 
-// The rows' losses, then (the workgroup that is done last) the sums, of
-// per-workgroup sums in a fixed order.
-template <typename T>
-__global__ __launch_bounds__(kRowsThreads) void distill_rows_kernel(const T* __restrict__ draft, DistillArgs a,
-                                                                    const Mass* __restrict__ parts, int32_t R,
-                                                                    float* __restrict__ kl, float* __restrict__ lse,
-                                                                    float* __restrict__ rest, uint8_t* __restrict__ flags,
-                                                                    float* __restrict__ sums, double* partial,
-                                                                    uint32_t* ticket) {
-  __shared__ int32_t sh_ids[kRowsWaves][DSPARK_MAX_TOP];
-  __shared__ double shs[3][kRowsWaves];
-  __shared__ uint32_t shl;
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  double num = 0.0, sum = 0.0, cnt = 0.0;
-  for (int64_t rr = static_cast<int64_t>(blockIdx.x) * kRowsWaves + wave; rr < R;
-       rr += static_cast<int64_t>(gridDim.x) * kRowsWaves) {
+// A row's outputs, by one wave; returns its loss as written.
+template <int ENT>
+__device__ __forceinline__ float finish_row(const Entries<ENT>& e, const DistillArgs& a, size_t row, double rest2,
+                                            int32_t* sh_ids, const LossOut& out) {
+  const Outcomes<ENT> o = outcomes<ENT>(e, a.K, rest2, a.c64, sh_ids);
+  double k = 0.0;
+#pragma unroll
+  for (int i = 0; i < ENT; ++i) {
+    const double t = exp2(o.lt[i]);
+    if (t > 0.0) k += t * (o.lt[i] - o.ls[i]);
+  }
+  k = wave_sum64(k);
+  const double tr = exp2(o.lt_r);
+  if (tr > 0.0) k += tr * (o.lt_r - o.ls_r);
+  const float nan = __builtin_nanf("");
+  const float loss = o.bad ? nan : o.empty ? 0.0f : static_cast<float>(k * kLn2d);
+  if ((threadIdx.x & 63) == 0) {
+    out.kl[row] = loss;
+    out.lse[row] = o.bad ? nan : static_cast<float>(o.lse * kLn2d);
+    out.rest[row] = o.bad ? nan : static_cast<float>(rest2 * kLn2d);
+    out.flags[row] = o.bad ? DSPARK_FLAG_NONFINITE : o.empty ? DSPARK_FLAG_EMPTY_ROW : 0;
+  }
+  return loss;
+}
+
+// One workgroup a row.
+template <typename T, int NT, int ENT>
+__global__ __launch_bounds__(NT, 4) void distill_loss_kernel(const T* __restrict__ draft, DistillArgs a, int32_t R,
+                                                             LossOut out) {
+  __shared__ uint32_t member[kMaxTiles * NT];
+  __shared__ __align__(16) int32_t sh_ids[64 * ENT];
+  __shared__ Mass shm[NT / 64];
+  for (int rr = blockIdx.x; rr < R; rr += gridDim.x) {
     const size_t row = static_cast<size_t>(rr);
     const Row<T> r = make_row(draft + row * a.V, a.V);
-    Mass m = mass_none();
-    for (int p = lane; p < a.P; p += 64) m = mass_add(m, parts[row * a.P + p], a.c);
-    m = wave_mass(m, a.c);
-    const double rest2 = mass_log2(m, a.c, a.c64);
-    const Outcomes o = outcomes(r, a.values, a.ids, a.teacher_rest, row, a.K, rest2, a.c64, sh_ids[wave]);
-    double k = 0.0;
-#pragma unroll
-    for (int i = 0; i < kEnt; ++i) {
-      if (i * 64 >= a.K) break;
-      const double t = exp2(o.lt[i]);
-      if (t > 0.0) k += t * (o.lt[i] - o.ls[i]);
-    }
-    k = wave_sum64(k);
-    const double tr = exp2(o.lt_r);
-    if (tr > 0.0) k += tr * (o.lt_r - o.ls_r);
-    const double loss = o.bad ? __builtin_nan("") : o.empty ? 0.0 : k * kLn2d;
-    if (lane == 0) {
-      kl[row] = static_cast<float>(loss);
-      lse[row] = o.bad ? __builtin_nanf("") : static_cast<float>(o.lse * kLn2d);
-      rest[row] = o.bad ? __builtin_nanf("") : static_cast<float>(rest2 * kLn2d);
-      flags[row] = o.bad ? DSPARK_FLAG_NONFINITE : o.empty ? DSPARK_FLAG_EMPTY_ROW : 0;
-    }
-    const int b = static_cast<int>(row / a.gamma), pos = static_cast<int>(row - static_cast<size_t>(b) * a.gamma);
-    if (!a.block_mask || a.block_mask[b]) {
-      num += exp(-static_cast<double>(pos + 1) / a.gamma) * loss;
-      sum += loss;
-      cnt += 1.0;
-    }
-  }
-  if (lane == 0) {
-    shs[0][wave] = num;
-    shs[1][wave] = sum;
-    shs[2][wave] = cnt;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double t[3] = {0.0, 0.0, 0.0};
-    for (int q = 0; q < 3; ++q)
-      for (int w = 0; w < kRowsWaves; ++w) t[q] += shs[q][w];
-    for (int q = 0; q < 3; ++q) {
-      const uint64_t v = static_cast<uint64_t>(__double_as_longlong(t[q]));
-      uint32_t* p = reinterpret_cast<uint32_t*>(partial + static_cast<size_t>(blockIdx.x) * 3 + q);
-      store_coherent(p, static_cast<uint32_t>(v));
-      store_coherent(p + 1, static_cast<uint32_t>(v >> 32));
-    }
-    shl = publish(ticket) == gridDim.x - 1 ? 1u : 0u;
-  }
-  __syncthreads();
-  if (shl && wave == 0) {
-    double t[3] = {0.0, 0.0, 0.0};
-    for (int i = lane; i < static_cast<int>(gridDim.x); i += 64)
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(partial + static_cast<size_t>(i) * 3 + q);
-        const uint64_t lo = load_coherent(p), hi = load_coherent(p + 1);
-        t[q] += __longlong_as_double(static_cast<long long>(lo | (hi << 32)));
-      }
-#pragma unroll
-    for (int q = 0; q < 3; ++q) t[q] = wave_sum64(t[q]);
-    if (lane == 0) {
-      sums[0] = static_cast<float>(a.weight * t[0]);
-      sums[1] = static_cast<float>(t[2]);
-      sums[2] = static_cast<float>(t[1]);
-      sums[3] = static_cast<float>(t[2]);
-    }
+    Entries<ENT> e;
+    if (wave_id() == 0) e = load_entries<T, ENT>(r, a, row);  // on their way while the row streams
+    const double rest2 = outside_mass<T, NT, kMaxTiles>(r, a, row, threadIdx.x, member, shm);
+    if (wave_id() == 0) finish_row<ENT>(e, a, row, rest2, sh_ids, out);
+    __syncthreads();  // LDS is reused by the next row
   }
 }
 
-// Sums of an empty batch.
-__global__ void distill_zero_kernel(float* sums) {
-  if (threadIdx.x < 4) sums[threadIdx.x] = 0.0f;
+// Row weights and sums.
+struct Sums {
+  double num, sum, cnt;
+};
+// Weights exp(-k / gamma) of the positions into LDS, by 16 threads; the caller
+// synchronises.
+__device__ __forceinline__ void position_weights(double* w, int32_t gamma) {
+  if (threadIdx.x < DSPARK_MAX_GAMMA) w[threadIdx.x] = exp(-static_cast<double>(threadIdx.x + 1) / gamma);
+}
+__device__ __forceinline__ void add_row(Sums& s, const DistillArgs& a, const double* w, size_t row, float loss) {
+  const uint32_t r = static_cast<uint32_t>(row), b = r / static_cast<uint32_t>(a.gamma);
+  if (a.block_mask && !a.block_mask[b]) return;
+  s.num += w[r - b * a.gamma] * loss;
+  s.sum += loss;
+  s.cnt += 1.0;
+}
+__device__ __forceinline__ void write_sums(float* sums, const Sums& s, float weight) {
+  sums[0] = static_cast<float>(weight * s.num);
+  sums[1] = static_cast<float>(s.cnt);
+  sums[2] = static_cast<float>(s.sum);
+  sums[3] = static_cast<float>(s.cnt);
+}
+
+// A few short rows: one workgroup, a wave a row, the sums included.
+template <typename T, int ENT>
+__global__ __launch_bounds__(kTinyThreads) void distill_tiny_kernel(const T* __restrict__ draft, DistillArgs a,
+                                                                    int32_t R, LossOut out, float* __restrict__ sums) {
+  __shared__ uint32_t member[kTinyWaves][kTinyTiles * 64];
+  __shared__ __align__(16) int32_t sh_ids[kTinyWaves][64 * ENT];
+  __shared__ Sums shs[kTinyWaves];
+  __shared__ double shw[DSPARK_MAX_GAMMA];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  position_weights(shw, a.gamma);
+  __syncthreads();
+  Sums s{0.0, 0.0, 0.0};
+  for (int rr = wave; rr < R; rr += kTinyWaves) {
+    const size_t row = static_cast<size_t>(rr);
+    const Row<T> r = make_row(draft + row * a.V, a.V);
+    const Entries<ENT> e = load_entries<T, ENT>(r, a, row);
+    const double rest2 = outside_mass<T, 64, kTinyTiles>(r, a, row, lane, member[wave], nullptr);
+    add_row(s, a, shw, row, finish_row<ENT>(e, a, row, rest2, sh_ids[wave], out));
+  }
+  if (lane == 0) shs[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Sums t{0.0, 0.0, 0.0};
+    for (int w = 0; w < kTinyWaves; ++w) {
+      t.num += shs[w].num;
+      t.sum += shs[w].sum;
+      t.cnt += shs[w].cnt;
+    }
+    write_sums(sums, t, a.weight);
+  }
+}
+
+// Sums of the rows' losses: a workgroup's stretch of rows, added in a fixed
+// order; several workgroups leave partial sums for distill_sums_final.
+__global__ __launch_bounds__(kSumThreads) void distill_sums_kernel(const float* __restrict__ kl, DistillArgs a,
+                                                                   int32_t R, int32_t stretch,
+                                                                   Sums* __restrict__ partial,
+                                                                   float* __restrict__ sums) {
+  __shared__ Sums shs[kSumThreads / 64];
+  __shared__ double shw[DSPARK_MAX_GAMMA];
+  position_weights(shw, a.gamma);
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * stretch;
+  const int64_t r1 = min(r0 + stretch, static_cast<int64_t>(R));
+  Sums s{0.0, 0.0, 0.0};
+  for (int64_t row = r0 + threadIdx.x; row < r1; row += kSumThreads)
+    add_row(s, a, shw, static_cast<size_t>(row), kl[row]);
+  s = Sums{wave_sum64(s.num), wave_sum64(s.sum), wave_sum64(s.cnt)};
+  if (lane == 0) shs[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Sums t{0.0, 0.0, 0.0};
+    for (int w = 0; w < kSumThreads / 64; ++w) {
+      t.num += shs[w].num;
+      t.sum += shs[w].sum;
+      t.cnt += shs[w].cnt;
+    }
+    if (gridDim.x == 1)
+      write_sums(sums, t, a.weight);
+    else
+      partial[blockIdx.x] = t;
+  }
+}
+__global__ __launch_bounds__(64) void distill_sums_final_kernel(const Sums* __restrict__ partial, int32_t n,
+                                                                float weight, float* __restrict__ sums) {
+  static_assert(kMaxSumBlocks <= 64, "a lane each");
+  const int lane = threadIdx.x;
+  const Sums p = lane < n ? partial[lane] : Sums{0.0, 0.0, 0.0};
+  const Sums s{wave_sum64(p.num), wave_sum64(p.sum), wave_sum64(p.cnt)};
+  if (lane == 0) write_sums(sums, s, weight);
 }
 
 // ---- gradient -------------------------------------------------------------------------
@@ -342,55 +431,62 @@ __device__ __forceinline__ void gran_store(T* g, const Row<T>& r, int q, bool ve
   }
 }
 
-template <typename T, int NT>
-__global__ __launch_bounds__(NT) void distill_grad_kernel(const T* __restrict__ draft, DistillArgs a,
-                                                          const float* __restrict__ rest,
-                                                          const float* __restrict__ grad_scale, int64_t items,
-                                                          int32_t tiles, T* __restrict__ grad) {
-  constexpr int EPL = Row<T>::EPL;
-  __shared__ int32_t sh_ids[DSPARK_MAX_TOP];  // tokens to write over
-  __shared__ float sh_d[DSPARK_MAX_TOP];
-  __shared__ double sh_t[DSPARK_MAX_TOP];
+// One segment of a row a workgroup: `groups` groups a thread.
+template <typename T, int NT, int ENT>
+__global__ __launch_bounds__(NT, 4) void distill_grad_kernel(const T* __restrict__ draft, DistillArgs a,
+                                                             const float* __restrict__ rest,
+                                                             const float* __restrict__ grad_scale, int64_t items,
+                                                             int32_t P, int32_t groups, T* __restrict__ grad) {
+  constexpr int EPL = Row<T>::EPL, L = group_granules<T>(), TILE = NT * L;
+  __shared__ __align__(16) int32_t sh_ids[64 * ENT];  // tokens to write over
+  __shared__ float sh_d[64 * ENT];
+  __shared__ double sh_t[64 * ENT];
   __shared__ float shc[2];  // factor, reference
   __shared__ int shf[2];    // a row of zeros; the reference is a logit
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const size_t row = static_cast<size_t>(item / a.P);
-    const int seg = static_cast<int>(item - static_cast<int64_t>(row) * a.P);
+    const size_t row = static_cast<size_t>(item / P);
+    const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
     const size_t b = row / a.gamma;
     const Row<T> r = make_row(draft + row * a.V, a.V);
     T* g = grad + row * a.V;
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
-    const int first = seg * tiles * (NT * kL);
-    const int n = min(tiles, (r.Q - first + NT * kL - 1) / (NT * kL));
+    const int first = seg * groups * TILE;
+    const int n = min(groups, (r.Q - first + TILE - 1) / TILE);
     const bool live = !a.block_mask || a.block_mask[b] != 0;
-    uint4 ua[kL], ub[kL];
-    if (live && n > 0) group_load<T, NT, kL>(r, first, tid, ua);
+    uint4 ua[L], ub[L];
+    if (live && n > 0) group_load<T, NT, L>(r, first, tid, ua);
     if (wave == 0) {
       bool zero = true;
       if (live) {
         const float rst = rest[row];
+        const float scale = grad_scale ? grad_scale[0] : 1.0f;
         const double rest2 = static_cast<double>(rst) * kLog2ed;
-        const Outcomes o = outcomes(r, a.values, a.ids, a.teacher_rest, row, a.K, rest2, a.c64, sh_ids);
-        const double w = (grad_scale ? static_cast<double>(grad_scale[0]) : 1.0) * a.weight * a.c64 / kLog2ed *
+        const Entries<ENT> e = load_entries<T, ENT>(r, a, row);
+        const Outcomes<ENT> o = outcomes<ENT>(e, a.K, rest2, a.c64, sh_ids);
+        const double w = static_cast<double>(scale) * a.weight * (a.c64 / kLog2ed) *
                          exp(-static_cast<double>(row - b * a.gamma + 1) / a.gamma);
         zero = o.empty && !o.bad;
+        double t[ENT];
 #pragma unroll
-        for (int i = 0; i < kEnt; ++i) sh_t[i * 64 + lane] = o.id[i] >= 0 ? exp2(o.lt[i]) : 0.0;
-        __builtin_amdgcn_wave_barrier();
-        __threadfence_block();
+        for (int i = 0; i < ENT; ++i) t[i] = e.id[i] >= 0 ? exp2(o.lt[i]) : 0.0;
+        if (o.twice) {
 #pragma unroll
-        for (int i = 0; i < kEnt; ++i) {
-          double t = 0.0;
-          for (int j = 0; j < a.K; ++j) t += sh_ids[j] == o.id[i] ? sh_t[j] : 0.0;
-          sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls[i]) - t));
+          for (int i = 0; i < ENT; ++i) sh_t[i * 64 + lane] = t[i];
+          row_sync<64>();
+#pragma unroll
+          for (int i = 0; i < ENT; ++i) {
+            t[i] = 0.0;
+            for (int j = 0; j < a.K; ++j) t[i] += sh_ids[j] == e.id[i] ? sh_t[j] : 0.0;
+          }
+          row_sync<64>();
         }
-        __builtin_amdgcn_wave_barrier();
-        __threadfence_block();
-        const int32_t e0 = first * EPL - r.head, e1 = (first + tiles * NT * kL) * EPL - r.head;  // of this segment
+        const int32_t e0 = first * EPL - r.head, e1 = (first + groups * TILE) * EPL - r.head;  // of this segment
 #pragma unroll
-        for (int i = 0; i < kEnt; ++i)
-          sh_ids[i * 64 + lane] = o.first[i] && o.id[i] >= e0 && o.id[i] < e1 ? o.id[i] : -1;
+        for (int i = 0; i < ENT; ++i) {
+          sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls[i]) - t[i]));
+          sh_ids[i * 64 + lane] = ((o.first >> i) & 1u) && e.id[i] >= e0 && e.id[i] < e1 ? e.id[i] : -1;
+        }
         if (lane == 0) {
           // the reference is rounded to fp32; what that loses goes into the factor
           float ref = static_cast<float>(rest2);
@@ -416,30 +512,32 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(const T* __restrict__ 
       const float z[EPL] = {};
       for (int t = 0; t < n; ++t)
 #pragma unroll
-        for (int i = 0; i < kL; ++i) {
-          const int q = first + (t * kL + i) * NT + tid;
+        for (int i = 0; i < L; ++i) {
+          const int q = first + (t * L + i) * NT + tid;
           if (q < r.Q) gran_store(g, r, q, vec, z);
         }
     } else {
       const bool huge = shf[1] != 0;
-      auto put = [&](const uint4(&u)[kL], int t) {
+      auto put = [&](const uint4(&u)[L], int t) {
 #pragma unroll
-        for (int i = 0; i < kL; ++i) {
-          const int q = first + (t * kL + i) * NT + tid;
+        for (int i = 0; i < L; ++i) {
+          const int q = first + (t * L + i) * NT + tid;
           float v[EPL];
+          if (huge) {
 #pragma unroll
-          for (int j = 0; j < EPL; ++j) {
-            const float x = gran_elem(u[i], j, T{});
-            v[j] = A * __builtin_amdgcn_exp2f(huge ? (x - ref) * a.c : fmaf(x, a.c, -ref));
+            for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f((gran_elem(u[i], j, T{}) - ref) * a.c);
+          } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f(fmaf(gran_elem(u[i], j, T{}), a.c, -ref));
           }
           if (q < r.Q) gran_store(g, r, q, vec, v);
         }
       };
       for (int t = 0; t < n; t += 2) {
-        if (t + 1 < n) group_load<T, NT, kL>(r, first + (t + 1) * NT * kL, tid, ub);
+        if (t + 1 < n) group_load<T, NT, L>(r, first + (t + 1) * TILE, tid, ub);
         put(ua, t);
         if (t + 1 >= n) break;
-        if (t + 2 < n) group_load<T, NT, kL>(r, first + (t + 2) * NT * kL, tid, ua);
+        if (t + 2 < n) group_load<T, NT, L>(r, first + (t + 2) * TILE, tid, ua);
         put(ub, t + 1);
       }
       __syncthreads();  // the listed tokens are written after the granules that hold them
@@ -450,101 +548,92 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(const T* __restrict__ 
   }
 }
 
-struct Split {
-  int NT, tiles, P;
-};
+// Granules of a row at the least favourable alignment.
+int row_granules(int epl, int32_t V) { return static_cast<int>((static_cast<int64_t>(V) + 2 * epl - 2) / epl); }
 
-// Rows of at most kMaxTiles groups of a wave are taken by waves; others by
-// workgroups of 256, in segments of at most kMaxTiles groups, shorter ones
-// where that fills the GPU.
-Split split(int epl, int64_t R, int32_t V) {
-  const int64_t q = (static_cast<int64_t>(V) + 2 * epl - 2) / epl;
-  Split s{};
-  s.NT = q <= 2 * 64 * kL ? 64 : 256;
-  const int64_t need = (q + s.NT * kL - 1) / (s.NT * kL);  // groups of a row
-  int t = static_cast<int>(std::min<int64_t>(kMaxTiles, need));
-  while (t > 1 && R * ((need + t - 1) / t) < 1024) t = (t + 1) / 2;
-  s.tiles = t;
-  s.P = static_cast<int>((need + t - 1) / t);
-  return s;
-}
-
-dim3 item_grid(int64_t items) { return dim3(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid))); }
-
-template <typename T>
-hipError_t launch_loss(const T* draft, const DistillArgs& a, const Split& s, int32_t R, float* kl, float* lse,
-                       float* rest, uint8_t* flags, float* sums, Mass* parts, double* partial, uint32_t* ticket,
+template <typename T, int ENT>
+hipError_t launch_loss(const T* draft, const DistillArgs& a, int32_t R, const LossOut& out, float* sums, Sums* partial,
                        hipStream_t st) {
-  const int64_t items = static_cast<int64_t>(R) * s.P;
-  if (s.NT == 64)
-    DSPARK_LAUNCH("distill_mass", (distill_mass_kernel<T, 64>), item_grid(items), dim3(64), 0, st, draft, a.ids, items,
-                  a.V, a.K, s.P, s.tiles, a.c, parts, ticket);
+  constexpr int L = group_granules<T>();
+  const int q = row_granules(Row<T>::EPL, a.V);
+  if (R <= 64 && q <= kTinyTiles * 64 * L) {
+    DSPARK_LAUNCH("distill_tiny", (distill_tiny_kernel<T, ENT>), dim3(1), dim3(kTinyThreads), 0, st, draft, a, R, out,
+                  sums);
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<unsigned>(std::min(R, kMaxGrid)));
+  if (q <= 2 * 64 * L)
+    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, R, out);
+  else if (R > 512 || q <= 4 * 256 * L)
+    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, R, out);
   else
-    DSPARK_LAUNCH("distill_mass", (distill_mass_kernel<T, 256>), item_grid(items), dim3(256), 0, st, draft, a.ids,
-                  items, a.V, a.K, s.P, s.tiles, a.c, parts, ticket);
-  const hipError_t e = hipGetLastError();
+    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 512, ENT>), grid, dim3(512), 0, st, draft, a, R, out);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int wgs = std::min(kRowsGrid, (R + kRowsWaves - 1) / kRowsWaves);
-  DSPARK_LAUNCH("distill_rows", (distill_rows_kernel<T>), dim3(wgs), dim3(kRowsThreads), 0, st, draft, a, parts, R, kl,
-                lse, rest, flags, sums, partial, ticket);
+  const int blocks = std::min(kMaxSumBlocks, (R + 16383) / 16384);
+  DSPARK_LAUNCH("distill_sums", distill_sums_kernel, dim3(blocks), dim3(kSumThreads), 0, st, out.kl, a, R,
+                (R + blocks - 1) / blocks, partial, sums);
+  if (blocks > 1)
+    DSPARK_LAUNCH("distill_sums_final", distill_sums_final_kernel, dim3(1), dim3(64), 0, st, partial, blocks, a.weight,
+                  sums);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_grad(const T* draft, const DistillArgs& a, const Split& s, int32_t R, const float* rest,
-                       const float* grad_scale, T* grad, hipStream_t st) {
-  const int64_t items = static_cast<int64_t>(R) * s.P;
-  if (s.NT == 64)
-    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 64>), item_grid(items), dim3(64), 0, st, draft, a, rest,
-                  grad_scale, items, s.tiles, grad);
+template <typename T, int ENT>
+hipError_t launch_grad(const T* draft, const DistillArgs& a, int32_t R, const float* rest, const float* grad_scale,
+                       T* grad, hipStream_t st) {
+  constexpr int L = group_granules<T>();
+  const int q = row_granules(Row<T>::EPL, a.V);
+  const int nt = q <= 2 * 64 * L ? 64 : 256;
+  const int need = (q + nt * L - 1) / (nt * L);  // groups of a thread over the row
+  int groups = need;  // shorter segments where that fills the GPU
+  while (groups > 1 && static_cast<int64_t>(R) * ((need + groups - 1) / groups) < 1024) groups = (groups + 1) / 2;
+  const int P = (need + groups - 1) / groups;
+  const int64_t items = static_cast<int64_t>(R) * P;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid)));
+  if (nt == 64)
+    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, rest, grad_scale,
+                  items, P, groups, grad);
   else
-    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 256>), item_grid(items), dim3(256), 0, st, draft, a, rest,
-                  grad_scale, items, s.tiles, grad);
+    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, rest,
+                  grad_scale, items, P, groups, grad);
   return hipGetLastError();
+}
+
+// Sums of an empty batch.
+__global__ void distill_zero_kernel(float* sums) {
+  if (threadIdx.x < 4) sums[threadIdx.x] = 0.0f;
 }
 
 DistillArgs distill_args(const float* values, const int32_t* ids, const float* teacher_rest, const uint8_t* block_mask,
-                         int32_t N, int32_t gamma, int32_t V, int32_t K, int32_t P, float temperature, float weight) {
-  return DistillArgs{values, ids, teacher_rest, block_mask, N, gamma, V, K, P, mass_scale(temperature),
+                         int32_t N, int32_t gamma, int32_t V, int32_t K, float temperature, float weight) {
+  return DistillArgs{values, ids, teacher_rest, block_mask, N, gamma, V, K, mass_scale(temperature),
                      mass_scale64(temperature), weight};
 }
 
 }  // namespace
 
-DistillPlan plan_distill(int32_t N, int32_t gamma, int32_t V) {
-  DistillPlan p{};
-  const int64_t R = static_cast<int64_t>(N) * gamma;
-  const int P = std::max(split(4, R, V).P, split(8, R, V).P);
-  size_t off = 0;
-  p.off_ticket = off;
-  off = align_up(off + sizeof(uint32_t), 256);
-  p.off_partial = off;
-  off = align_up(off + static_cast<size_t>(kRowsGrid) * 3 * sizeof(double), 256);
-  p.off_parts = off;
-  off = align_up(off + static_cast<size_t>(R) * P * sizeof(Mass), 256);
-  p.bytes = off;
-  return p;
-}
+size_t distill_bytes() { return align_up(kMaxSumBlocks * sizeof(Sums), 256); }
 
 hipError_t launch_distill(const void* draft, int dtype, const float* values, const int32_t* ids,
                           const float* teacher_rest, const uint8_t* block_mask, int32_t N, int32_t gamma, int32_t V,
                           int32_t K, float temperature, float weight, float* kl, float* lse, float* rest,
-                          uint8_t* flags, float* sums, void* ws, const DistillPlan& pl, hipStream_t st) {
+                          uint8_t* flags, float* sums, void* ws, hipStream_t st) {
   const int32_t R = N * gamma;
   if (R == 0) {
     DSPARK_LAUNCH("distill_zero", distill_zero_kernel, dim3(1), dim3(64), 0, st, sums);
     return hipGetLastError();
   }
-  char* w = static_cast<char*>(ws);
-  Mass* parts = reinterpret_cast<Mass*>(w + pl.off_parts);
-  double* partial = reinterpret_cast<double*>(w + pl.off_partial);
-  uint32_t* ticket = reinterpret_cast<uint32_t*>(w + pl.off_ticket);
-  const Split s = split(dtype == DSPARK_BF16 ? 8 : 4, R, V);
-  const DistillArgs a = distill_args(values, ids, teacher_rest, block_mask, N, gamma, V, K, s.P, temperature, weight);
+  Sums* partial = static_cast<Sums*>(ws);
+  const LossOut out{kl, lse, rest, flags};
+  const DistillArgs a = distill_args(values, ids, teacher_rest, block_mask, N, gamma, V, K, temperature, weight);
+  const uint16_t* h = static_cast<const uint16_t*>(draft);
+  const float* f = static_cast<const float*>(draft);
   if (dtype == DSPARK_BF16)
-    return launch_loss(static_cast<const uint16_t*>(draft), a, s, R, kl, lse, rest, flags, sums, parts, partial,
-                       ticket, st);
-  return launch_loss(static_cast<const float*>(draft), a, s, R, kl, lse, rest, flags, sums, parts, partial, ticket, st);
+    return K <= 64 ? launch_loss<uint16_t, 1>(h, a, R, out, sums, partial, st)
+                   : launch_loss<uint16_t, 2>(h, a, R, out, sums, partial, st);
+  return K <= 64 ? launch_loss<float, 1>(f, a, R, out, sums, partial, st)
+                 : launch_loss<float, 2>(f, a, R, out, sums, partial, st);
 }
 
 hipError_t launch_distill_backward(const void* draft, int dtype, const float* values, const int32_t* ids,
@@ -552,12 +641,16 @@ hipError_t launch_distill_backward(const void* draft, int dtype, const float* va
                                    int32_t gamma, int32_t V, int32_t K, float temperature, float weight,
                                    const float* grad_scale, void* grad_draft, hipStream_t st) {
   const int32_t R = N * gamma;
-  const Split s = split(dtype == DSPARK_BF16 ? 8 : 4, R, V);
-  const DistillArgs a = distill_args(values, ids, teacher_rest, block_mask, N, gamma, V, K, s.P, temperature, weight);
+  const DistillArgs a = distill_args(values, ids, teacher_rest, block_mask, N, gamma, V, K, temperature, weight);
+  const uint16_t* h = static_cast<const uint16_t*>(draft);
+  const float* f = static_cast<const float*>(draft);
+  uint16_t* gh = static_cast<uint16_t*>(grad_draft);
+  float* gf = static_cast<float*>(grad_draft);
   if (dtype == DSPARK_BF16)
-    return launch_grad(static_cast<const uint16_t*>(draft), a, s, R, rest, grad_scale,
-                       static_cast<uint16_t*>(grad_draft), st);
-  return launch_grad(static_cast<const float*>(draft), a, s, R, rest, grad_scale, static_cast<float*>(grad_draft), st);
+    return K <= 64 ? launch_grad<uint16_t, 1>(h, a, R, rest, grad_scale, gh, st)
+                   : launch_grad<uint16_t, 2>(h, a, R, rest, grad_scale, gh, st);
+  return K <= 64 ? launch_grad<float, 1>(f, a, R, rest, grad_scale, gf, st)
+                 : launch_grad<float, 2>(f, a, R, rest, grad_scale, gf, st);
 }
 
 }  // namespace dspark

@@ -172,22 +172,18 @@ TopPlan plan_top(int32_t R, int32_t V, int32_t K);
 hipError_t launch_top(const void* logits, int dtype, int32_t R, int32_t V, int32_t K, float temperature, float* values,
                       int32_t* ids, float* rest, float* lse, uint8_t* flags, void* ws, const TopPlan& pl,
                       hipStream_t st);
-// Per beam a list of top_list_len(M) candidates that holds its M best: the order
-// keys of their 64-bit scores and their keys; and the beams' flags.
-int top_list_len(int K);
+// Per beam its M best candidates in order: the order keys of their 64-bit scores
+// and their keys (0: none); and the beams' flags.
 hipError_t launch_beam_rows(const void* logits, int dtype, int32_t R, int32_t V, int32_t M, const float* scores,
                             const uint8_t* finished, int32_t eos, uint64_t* sums, uint64_t* keys, uint8_t* flags,
                             void* ws, const TopPlan& pl, hipStream_t st);
 
 // ---- distillation from a teacher's highest logits (distill.hip) ----
-struct DistillPlan {
-  size_t off_ticket, off_partial, off_parts, bytes;
-};
-DistillPlan plan_distill(int32_t N, int32_t gamma, int32_t V);
+size_t distill_bytes();  // workspace of the loss
 hipError_t launch_distill(const void* draft, int dtype, const float* values, const int32_t* ids,
                           const float* teacher_rest, const uint8_t* block_mask, int32_t N, int32_t gamma, int32_t V,
                           int32_t K, float temperature, float weight, float* kl, float* lse, float* rest,
-                          uint8_t* flags, float* sums, void* ws, const DistillPlan& pl, hipStream_t st);
+                          uint8_t* flags, float* sums, void* ws, hipStream_t st);
 hipError_t launch_distill_backward(const void* draft, int dtype, const float* values, const int32_t* ids,
                                    const float* rest, const float* teacher_rest, const uint8_t* block_mask, int32_t N,
                                    int32_t gamma, int32_t V, int32_t K, float temperature, float weight,

@@ -86,6 +86,12 @@ __device__ __forceinline__ void group_load(const Row<T>& r, int q0, int tid, uin
   }
 }
 
+// Granules of a group: 32 logits.
+template <typename T>
+constexpr int group_granules() {
+  return sizeof(T) == 2 ? 4 : 8;
+}
+
 // ---- masses ----------------------------------------------------------------------
 // A mass is sum exp(x / T) held as (m, s): s = sum 2^(x c - fl(m c)), with m
 // the largest x, c = fl(log2(e) / T) and fl the rounding to fp32 (one fused

@@ -5,7 +5,7 @@
 // natural logarithm of sum exp(x / T) over the other tokens and over all.
 //
 // One pass over the row.  A workgroup takes a segment of a row, every thread
-// up to 16 groups of 4 granules (32 bf16 or 16 fp32 logits), and keeps of each
+// up to 16 groups of 32 logits, and keeps of each
 // group its maximum and its mass (rowstream.hpp) in LDS: one exponential and
 // about 7.5 VALU slots per element, no running maximum and no candidate test in
 // the stream.  K or a few more of the threads' maxima (of the groups' where K
@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kMergeThreads = 256;
 constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch; each then takes several items
-constexpr int kL = 4;              // granules of a group
 
 // Groups of a thread at most (they are kept in LDS) and keys that are ranked at
 // once: more are first cut by a search.
@@ -62,7 +61,7 @@ struct TopOut {
   float* rest;     // [R]
   float* lse;      // [R]
   uint8_t* flags;  // [R]
-  uint64_t* keys;  // [R, P, list_len(K)]: a segment's candidates, 0: none
+  uint64_t* keys;  // a segment's candidates [R, P, list_len(K)], or a beam's K best in order [R, K]; 0: none
   Mass* parts;     // [R, P]: the mass of its other elements
 };
 
@@ -72,7 +71,7 @@ struct TopBeams {
   const float* scores;      // [R]
   const uint8_t* finished;  // [R] or NULL
   int32_t eos;
-  uint64_t* sums;  // [R, list_len(K)]: order keys of the candidates' 64-bit scores
+  uint64_t* sums;  // [R, K]: order keys of the candidates' 64-bit scores
   uint8_t* flags;  // [R]
 };
 
@@ -86,11 +85,10 @@ __device__ __forceinline__ bool unread_beam(const TopBeams& bm, const TopOut& o,
   if (sc > neg_inf() && sc < pos_inf() && !ended) return false;
   if constexpr (MODE == kBeams) {
     const bool fine = sc > neg_inf() && sc < pos_inf();
-    const int len = list_len(K);
-    for (int j = threadIdx.x; j < len; j += NT) {
+    for (int j = threadIdx.x; j < K; j += NT) {
       const bool one = fine && j == 0;
-      bm.sums[row * len + j] = order_key(one ? static_cast<double>(sc) : -__builtin_inf());
-      o.keys[row * len + j] = one ? cand_key(0, bm.eos) : 0;
+      bm.sums[row * K + j] = one ? order_key(static_cast<double>(sc)) : kKey64NegInf;
+      o.keys[row * K + j] = one ? cand_key(0, bm.eos) : 0;
     }
     if (threadIdx.x == 0) bm.flags[row] = isnan(sc) || sc == pos_inf() ? DSPARK_FLAG_NONFINITE : 0;
   }
@@ -164,27 +162,24 @@ __device__ __forceinline__ void write_row(const TopOut& o, size_t row, const uin
   }
 }
 
-// A beam's candidates from its n keys and the mass of its other tokens (by the
-// first wave): the normaliser in 64 bits, the listed tokens one by one.
-__device__ __forceinline__ void write_beam(const TopBeams& bm, const TopOut& o, size_t row, const uint64_t* list, int n,
+// A beam's candidates from its sorted keys and the mass of its other tokens (by
+// the first wave): the normaliser in 64 bits, the listed tokens one by one.
+__device__ __forceinline__ void write_beam(const TopBeams& bm, const TopOut& o, size_t row, const uint64_t* sorted,
                                            int K, Mass others, bool bad, float c, double c64) {
-  const int lane = threadIdx.x, len = list_len(K);
-  if (bad) n = 0;
-  float top = neg_inf();
-  for (int j = lane; j < n; j += 64)
-    if (list[j]) top = fmaxf(top, key_value(list[j]));
-  const double ref = static_cast<double>(wave_max(top));
+  const int lane = threadIdx.x;
+  const uint64_t best = bad ? 0 : sorted[0];
+  const double ref = best ? static_cast<double>(key_value(best)) : 0.0;
   double sum = 0.0;
-  for (int j = lane; j < n; j += 64)
-    if (list[j]) sum += exp2((static_cast<double>(key_value(list[j])) - ref) * c64);
+  for (int j = lane; j < K; j += 64)
+    if (sorted[j]) sum += exp2((static_cast<double>(key_value(sorted[j])) - ref) * c64);
   sum = wave_sum64(sum) + exp2(mass_log2(others, c, c64) - ref * c64);
   const double lse = ref + log2(sum) / c64, sc = static_cast<double>(bm.scores[row]);
-  for (int j = lane; j < len; j += 64) {
-    const uint64_t k = j < n ? list[j] : 0;
-    bm.sums[row * len + j] = k ? order_key(sc + (static_cast<double>(key_value(k)) - lse)) : kKey64NegInf;
-    o.keys[row * len + j] = k;
+  for (int j = lane; j < K; j += 64) {
+    const uint64_t k = bad ? 0 : sorted[j];
+    bm.sums[row * K + j] = k ? order_key(sc + (static_cast<double>(key_value(k)) - lse)) : kKey64NegInf;
+    o.keys[row * K + j] = k;
   }
-  if (lane == 0) bm.flags[row] = bad ? DSPARK_FLAG_NONFINITE : ref == -__builtin_inf() ? DSPARK_FLAG_EMPTY_ROW : 0;
+  if (lane == 0) bm.flags[row] = bad ? DSPARK_FLAG_NONFINITE : best == 0 ? DSPARK_FLAG_EMPTY_ROW : 0;
 }
 
 // Mass of a granule's elements for which keep(value, index) holds.
@@ -305,7 +300,7 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
                                                             int32_t K, int32_t P, int32_t groups, float c, double c64,
                                                             TopBeams bm, TopOut o) {
   constexpr int NW = NT / 64;
-  constexpr int EPL = Row<T>::EPL;
+  constexpr int EPL = Row<T>::EPL, kL = group_granules<T>();
   constexpr int TILE = NT * kL;  // granules of a group over the workgroup
   __shared__ TopLds<NT> s;
   constexpr int QUAL = sizeof(s.qual) / sizeof(uint16_t), CAND = TopLds<NT>::kCand;
@@ -460,7 +455,7 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
 
       // ---- the K best of them or a few more; the others' mass ----
       nl = nc;
-      if (nc > (MODE == kRows ? TopCaps<NT>::kRank : list_len(K))) {
+      if (nc > (MODE == kLists ? list_len(K) : TopCaps<NT>::kRank)) {
         const uint64_t t = list_bound<NT>(s.cand, nc, nc, K, static_cast<uint64_t>(bound) << 32,
                                           static_cast<uint64_t>(kmax + 1) << 32, s.slots, step);
         mine = 0;
@@ -477,13 +472,13 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
         __syncthreads();
         list = s.list;
       }
-      if constexpr (MODE == kRows) {
+      if constexpr (MODE != kLists) {
         rank_keys<NT>(list, nl, K, s.sorted);
         const uint64_t kth = s.sorted[K - 1];  // 0: fewer than K, all of them are in
         for (int i = tid; i < nl; i += NT)
           if (list[i] < kth) others = mass_add(others, Mass{key_value(list[i]), 1.0f}, c);
       }
-    } else if constexpr (MODE == kRows) {
+    } else if constexpr (MODE != kLists) {
       for (int j = tid; j < K; j += NT) s.sorted[j] = 0;
     }
     if constexpr (MODE == kLists) {
@@ -503,7 +498,7 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
     if constexpr (MODE == kRows) {
       if (wave == 0) write_row(o, row, s.sorted, K, others, bad, c, c64);
     } else if constexpr (MODE == kBeams) {
-      if (wave == 0) write_beam(bm, o, row, list, nl, K, others, bad, c, c64);
+      if (wave == 0) write_beam(bm, o, row, s.sorted, K, others, bad, c, c64);
     } else {
       if (tid == 0) o.parts[row * P + seg] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
     }
@@ -522,7 +517,7 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
                                                        float c, double c64, TopBeams bm, TopOut o) {
   constexpr int EPL = Row<T>::EPL;
   __shared__ uint64_t cand[kSmallCand + 4];
-  __shared__ uint64_t sorted[kMaxList];
+  __shared__ uint64_t sorted[DSPARK_MAX_TOP];
   const int lane = threadIdx.x;
   int step = 0;
   for (int row = blockIdx.x; row < R; row += gridDim.x) {
@@ -542,7 +537,6 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
     const float wmax = wave_max(lmax);
     bool bad = wmax == pos_inf(), slow = false;
     Mass others = mass_none();
-    uint64_t* list = cand;
     int nl = 0;  // candidates listed
     if (!bad && wmax > neg_inf()) {
       // ---- bound: at least K granules (or all finite ones) reach it ----
@@ -598,25 +592,6 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
           }
         }
         __syncthreads();
-        if (MODE == kBeams && nl > list_len(K)) {
-          const uint64_t t = list_bound<64>(cand, nl, nl, K, static_cast<uint64_t>(bound) << 32,
-                                            static_cast<uint64_t>(kmax + 1) << 32, nullptr, step);
-          mine = 0;
-          for (int i = lane; i < nl; i += 64) mine += cand[i] >= t;
-          int n;
-          pos = block_scan<1>(mine, nullptr, n);
-          for (int i = lane; i < nl; i += 64) {
-            const uint64_t k = cand[i];
-            if (k >= t) {
-              sorted[pos++] = k;
-            } else {
-              others = mass_add(others, Mass{key_value(k), 1.0f}, c);
-            }
-          }
-          __syncthreads();
-          list = sorted;
-          nl = n;
-        }
       }
     }
     if (!slow) {
@@ -628,18 +603,16 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
         others = mass_add(others, group_mass<T, 4>(v, c), c);
       }
     }
-    if constexpr (MODE == kRows) {
-      rank_keys<64>(cand, nl, K, sorted);
-      const uint64_t kth = sorted[K - 1];
-      for (int i = lane; i < nl; i += 64)
-        if (cand[i] < kth) others = mass_add(others, Mass{key_value(cand[i]), 1.0f}, c);
-    }
+    rank_keys<64>(cand, nl, K, sorted);
+    const uint64_t kth = sorted[K - 1];
+    for (int i = lane; i < nl; i += 64)
+      if (cand[i] < kth) others = mass_add(others, Mass{key_value(cand[i]), 1.0f}, c);
     others = wave_mass(others, c);
     bad |= !(others.s >= 0.0f);
     if constexpr (MODE == kRows)
       write_row(o, at_row, sorted, K, others, bad, c, c64);
     else
-      write_beam(bm, o, at_row, list, nl, K, others, bad, c, c64);
+      write_beam(bm, o, at_row, sorted, K, others, bad, c, c64);
     __syncthreads();  // LDS is reused by the next row
   }
 }
@@ -693,7 +666,7 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
     }
     uint64_t* best = all;
     int nl = n;
-    if (n > (MODE == kRows ? 2 * list_len(K) : list_len(K))) {
+    if (n > 2 * list_len(K)) {
       const uint64_t t = list_bound<NT>(all, n, found, K, found ? low : 1, top + 1, slots, step);
       int mine = 0;
       for (int i = tid; i < n; i += NT) mine += all[i] >= t;
@@ -709,12 +682,10 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
       __syncthreads();
       best = list;
     }
-    if constexpr (MODE == kRows) {
-      rank_keys<NT>(best, nl, K, sorted);
-      const uint64_t kth = sorted[K - 1];
-      for (int i = tid; i < nl; i += NT)
-        if (best[i] != 0 && best[i] < kth) others = mass_add(others, Mass{key_value(best[i]), 1.0f}, c);
-    }
+    rank_keys<NT>(best, nl, K, sorted);
+    const uint64_t kth = sorted[K - 1];
+    for (int i = tid; i < nl; i += NT)
+      if (best[i] != 0 && best[i] < kth) others = mass_add(others, Mass{key_value(best[i]), 1.0f}, c);
     others = wave_mass(others, c);
     if (lane == 0) shm[wave] = others;
     __syncthreads();
@@ -724,7 +695,7 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
       if constexpr (MODE == kRows)
         write_row(o, at, sorted, K, others, bad, c, c64);
       else
-        write_beam(bm, o, at, best, nl, K, others, bad, c, c64);
+        write_beam(bm, o, at, sorted, K, others, bad, c, c64);
     }
     __syncthreads();
   }
@@ -735,6 +706,7 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
 TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
   // granules of a row, at the least favourable alignment
   const int q = any ? (V + 2 * epl - 2) / epl : V / epl;
+  const int kL = 32 / epl;
   TopSplit s{};
   s.P = 1;
   if (q <= 8 * 64) {
@@ -824,7 +796,6 @@ bool any_alignment(const void* p, int32_t V, int epl) {
 
 float mass_scale(float temperature) { return static_cast<float>(1.4426950408889634074 / static_cast<double>(temperature)); }
 double mass_scale64(float temperature) { return 1.4426950408889634074 / static_cast<double>(temperature); }
-int top_list_len(int K) { return list_len(K); }
 
 // Sized for either type and any alignment of the rows.
 TopPlan plan_top(int32_t R, int32_t V, int32_t K) {
