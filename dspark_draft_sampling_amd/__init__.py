@@ -468,6 +468,18 @@ def dspark_select_width(confidence, cost, want_expected=True, out=None):
     return out
 
 
+# The current stream's handle; without the raw accessor by way of a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _want(t, dtype, name, shape, device):
+    """_dev_tensor with everything given, cheap where all is well."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _dev_tensor(t, dtype, name, shape, device)
+
+
 class _on:
     """The launch context of one call: its device is the current one inside (and
     only switched to if it is not), stream is the device's current stream."""
@@ -483,7 +495,7 @@ class _on:
         if torch.cuda.current_device() != d.index:
             self._guard = torch.cuda.device(d)
             self._guard.__enter__()
-        self.stream = torch.cuda.current_stream(d).cuda_stream
+        self.stream = _raw_stream(d.index)
         return self
 
     def __exit__(self, *exc):
@@ -522,7 +534,10 @@ def _outputs(what, spec, out, device):
     """The output tensors of (name, dtype, shape): allocated, or the caller's, checked."""
     if out is None:
         return {name: torch.empty(shape, dtype=dtype, device=device) for name, dtype, shape in spec}
-    _check_out(out, spec, device, what)
+    for name, dtype, shape in spec:
+        t = out.get(name)
+        if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+            _check_out(out, spec, device, what)
     return out
 
 
@@ -548,8 +563,9 @@ def dspark_top_logits(logits, k, temperature=1.0, out=None):
     dev = logits.device
     with _on(dev) as c:
         out = _outputs("top_logits", [("top_values", torch.float32, (*lead, k)),
-                                      ("top_ids", torch.int32, (*lead, k)), ("rest", torch.float32, lead),
-                                      ("lse", torch.float32, lead), ("flags", torch.uint8, lead)], out, dev)
+                                      ("top_ids", torch.int32, (*lead, k)), ("rest", torch.float32, tuple(lead)),
+                                      ("lse", torch.float32, tuple(lead)),
+                                      ("flags", torch.uint8, tuple(lead))], out, dev)
         ws, nb = c.scratch(DSPARK_OP_TOP, R, 1, V, k)
         rc = lib().dspark_top_logits(_a(logits), dt, R, V, k, float(temperature), _a(out["top_values"]),
                                      _a(out["top_ids"]), _a(out["rest"]), _a(out["lse"]),
@@ -566,16 +582,15 @@ def _distill_args(what, draft, values, ids, teacher_rest, block_mask):
         raise DSparkError(f"{what}: draft must be [N, gamma, V]")
     N, g, V = draft.shape
     dev = draft.device
-    _dev_tensor(values, torch.float32, "teacher_values", device=dev)
-    if values.dim() != 3:
+    if not isinstance(values, torch.Tensor) or values.dim() != 3:
         raise DSparkError(f"{what}: teacher_values must be [N, gamma, K]")
     K = values.shape[2]
-    _dev_tensor(values, torch.float32, "teacher_values", (N, g, K))
-    _dev_tensor(ids, torch.int32, "teacher_ids", (N, g, K), dev)
+    _want(values, torch.float32, "teacher_values", (N, g, K), dev)
+    _want(ids, torch.int32, "teacher_ids", (N, g, K), dev)
     if teacher_rest is not None:
-        _dev_tensor(teacher_rest, torch.float32, "teacher_rest", (N, g), dev)
+        _want(teacher_rest, torch.float32, "teacher_rest", (N, g), dev)
     if block_mask is not None:
-        _dev_tensor(block_mask, torch.uint8, "block_mask", (N,), dev)
+        _want(block_mask, torch.uint8, "block_mask", (N,), dev)
     return dt, N, g, V, K
 
 
@@ -609,7 +624,7 @@ def dspark_distill_backward(draft, teacher_values, teacher_ids, rest, teacher_re
     dt, N, g, V, K = _distill_args("distill_backward", draft, teacher_values, teacher_ids, teacher_rest,
                                    block_mask)
     dev = draft.device
-    _dev_tensor(rest, torch.float32, "rest", (N, g), dev)
+    _want(rest, torch.float32, "rest", (N, g), dev)
     if grad_scale is not None:
         _dev_tensor(grad_scale, torch.float32, "grad_scale", device=dev)
         if grad_scale.numel() != 1:
@@ -639,9 +654,9 @@ def dspark_beam_select(logits, scores, picks, finished=None, eos_token=0, out=No
     if M < 0:
         raise DSparkError("beam_select: picks must be positive")
     dev = logits.device
-    _dev_tensor(scores, torch.float32, "scores", (B, W), dev)
+    _want(scores, torch.float32, "scores", (B, W), dev)
     if finished is not None:
-        _dev_tensor(finished, torch.uint8, "finished", (B, W), dev)
+        _want(finished, torch.uint8, "finished", (B, W), dev)
     with _on(dev) as c:
         out = _outputs("beam_select", [("tokens", torch.int32, (B, M)), ("parents", torch.int32, (B, M)),
                                        ("scores", torch.float32, (B, M)), ("flags", torch.uint8, (B, W))],

@@ -32,7 +32,7 @@ constexpr int kRankAll = 128;   // candidates ranked at once; more are first cut
 constexpr int kMaxGrid = 1 << 20;
 
 __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ sums,
-                                                                   const uint64_t* __restrict__ keys, int32_t B,
+                                                                   const uint64_t* __restrict__ keys, int32_t base,
                                                                    int32_t W, int32_t M,
                                                                    int32_t* __restrict__ tokens,
                                                                    int32_t* __restrict__ parents,
@@ -41,96 +41,94 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
   __shared__ uint64_t sh_sum[kMaxCand + 4];
   __shared__ uint64_t sh_best[kMaxCand + 4];
   __shared__ uint16_t sh_from[kMaxCand];
-  __shared__ int slots[6 * NW];
+  __shared__ uint64_t slots[2 * NW];
   __shared__ int scan[2][NW];
   __shared__ uint64_t red[2][NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int n = W * M;
   const int each = (n + NT - 1) / NT;  // a thread's stretch, so that positions keep their order
   int step = 0;
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    const uint64_t* key = keys + static_cast<size_t>(b) * n;
-    // ---- the candidates that there are, in order ----
-    uint64_t top = 0, low = ~0ull;
-    int mine = 0, found;
-    for (int i = tid; i < n; i += NT) {
-      const uint64_t d = sums[static_cast<size_t>(b) * n + i];
-      sh_sum[i] = d;
-      if (d > kKey64NegInf) {
-        ++mine;
-        top = max(top, d);
-        low = min(low, d);
-      }
+  const int b = base + static_cast<int>(blockIdx.x);
+  const uint64_t* key = keys + static_cast<size_t>(b) * n;
+  // ---- the candidates that there are, in order ----
+  uint64_t top = 0, low = ~0ull;
+  int mine = 0, found;
+  for (int i = tid; i < n; i += NT) {
+    const uint64_t d = sums[static_cast<size_t>(b) * n + i];
+    sh_sum[i] = d;
+    if (d > kKey64NegInf) {
+      ++mine;
+      top = max(top, d);
+      low = min(low, d);
     }
+  }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
-      low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
-    }
-    if (lane == 0) {
-      red[0][wave] = top;
-      red[1][wave] = low;
-    }
-    block_scan<NW>(mine, scan[0], found);  // its barrier completes sh_sum and red
-    uint64_t bound = kKey64NegInf + 1;
-    if (found > kRankAll) {
+  for (int d = 1; d < 64; d <<= 1) {
+    top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
+    low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
+  }
+  if (lane == 0) {
+    red[0][wave] = top;
+    red[1][wave] = low;
+  }
+  block_scan<NW>(mine, scan[0], found);  // its barrier completes sh_sum and red
+  uint64_t bound = kKey64NegInf + 1;
+  if (found > kRankAll) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        top = max(top, red[0][w]);
-        low = min(low, red[1][w]);
-      }
-      int n_lo = found;
-      bound = search_key<uint64_t>(low, top + 1, n_lo, M, M + M / 4 + 8, [&](uint64_t t1, uint64_t t2, uint64_t t3) {
-        Count3 k{0, 0, 0};
-        for (int i = tid; i < (n + 63) / 64 * 64; i += NT) {
-          const uint64_t d = i < n ? sh_sum[i] : 0;
-          k.a += __popcll(__ballot(d >= t1));
-          k.b += __popcll(__ballot(d >= t2));
-          k.c += __popcll(__ballot(d >= t3));
-        }
-        return block_count<NW>(k, slots, step);
-      });
+    for (int w = 0; w < NW; ++w) {
+      top = max(top, red[0][w]);
+      low = min(low, red[1][w]);
     }
-    // ---- those that can be among the M ----
-    int nb;
-    mine = 0;
-    const int i0 = tid * each, i1 = min(n, i0 + each);
-    for (int i = i0; i < i1; ++i) mine += sh_sum[i] >= bound;
-    int pos = block_scan<NW>(mine, scan[1], nb);
-    for (int i = i0; i < i1; ++i)
-      if (sh_sum[i] >= bound) {
-        sh_best[pos] = sh_sum[i];
-        sh_from[pos++] = static_cast<uint16_t>(i);
+    int n_lo = found;
+    bound = search_key<uint64_t>(low, top + 1, n_lo, M, M + M / 4 + 8, [&](uint64_t t1, uint64_t t2, uint64_t t3) {
+      Count3 k{0, 0, 0};
+      for (int i = tid; i < (n + 63) / 64 * 64; i += NT) {
+        const uint64_t d = i < n ? sh_sum[i] : 0;
+        k.a += __popcll(__ballot(d >= t1));
+        k.b += __popcll(__ballot(d >= t2));
+        k.c += __popcll(__ballot(d >= t3));
       }
-    if (tid < 4) sh_best[nb + tid] = 0;
-    __syncthreads();
-    // ---- rank: score, then position, which is beam, logit, token ----
-    for (int i = tid; i < nb; i += NT) {
-      const uint64_t d = sh_best[i];
-      int rank = 0;
-      for (int j = 0; j < nb; j += 4) {
-        const uint64_t d0 = sh_best[j], d1 = sh_best[j + 1], d2 = sh_best[j + 2], d3 = sh_best[j + 3];
-        rank += d0 > d - (j < i) ? 1 : 0;
-        rank += d1 > d - (j + 1 < i) ? 1 : 0;
-        rank += d2 > d - (j + 2 < i) ? 1 : 0;
-        rank += d3 > d - (j + 3 < i) ? 1 : 0;
-      }
-      if (rank < M) {
-        const int from = sh_from[i];
-        const uint64_t k = key[from];
-        const size_t o = static_cast<size_t>(b) * M + rank;
-        tokens[o] = key_index(k);
-        parents[o] = from / M;
-        scores[o] = static_cast<float>(key_double(d));
-      }
+      return block_count<NW>(k, slots, step);
+    });
+  }
+  // ---- those that can be among the M ----
+  int nb;
+  mine = 0;
+  const int i0 = tid * each, i1 = min(n, i0 + each);
+  for (int i = i0; i < i1; ++i) mine += sh_sum[i] >= bound;
+  int pos = block_scan<NW>(mine, scan[1], nb);
+  for (int i = i0; i < i1; ++i)
+    if (sh_sum[i] >= bound) {
+      sh_best[pos] = sh_sum[i];
+      sh_from[pos++] = static_cast<uint16_t>(i);
     }
-    for (int j = found + tid; j < M; j += NT) {  // fewer candidates than picks
-      const size_t o = static_cast<size_t>(b) * M + j;
-      tokens[o] = -1;
-      parents[o] = -1;
-      scores[o] = neg_inf();
+  if (tid < 4) sh_best[nb + tid] = 0;
+  __syncthreads();
+  // ---- rank: score, then position, which is beam, logit, token ----
+  for (int i = tid; i < nb; i += NT) {
+    const uint64_t d = sh_best[i];
+    int rank = 0;
+    for (int j = 0; j < nb; j += 4) {
+      const uint64_t d0 = sh_best[j], d1 = sh_best[j + 1], d2 = sh_best[j + 2], d3 = sh_best[j + 3];
+      rank += d0 > d - (j < i) ? 1 : 0;
+      rank += d1 > d - (j + 1 < i) ? 1 : 0;
+      rank += d2 > d - (j + 2 < i) ? 1 : 0;
+      rank += d3 > d - (j + 3 < i) ? 1 : 0;
     }
-    __syncthreads();  // LDS is reused by the next request
+    if (rank < M) {
+      const int from = sh_from[i];
+      const uint64_t k = key[from];
+      const size_t o = static_cast<size_t>(b) * M + rank;
+      tokens[o] = key_index(k);
+      parents[o] = from / M;
+      scores[o] = static_cast<float>(key_double(d));
+    }
+  }
+  for (int j = found + tid; j < M; j += NT) {  // fewer candidates than picks
+    const size_t o = static_cast<size_t>(b) * M + j;
+    tokens[o] = -1;
+    parents[o] = -1;
+    scores[o] = neg_inf();
   }
 }
 
@@ -230,8 +228,11 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
   const hipError_t e = launch_beam_rows(logits, dtype, B * W, V, M, scores, finished, eos, sums, keys, flags,
                                         w + pl.off_rows, pl.rows, st);
   if (e != hipSuccess) return e;
-  DSPARK_LAUNCH("beam_final", beam_final_kernel, dim3(static_cast<unsigned>(std::min(B, kMaxGrid))),
-                dim3(kFinalThreads), 0, st, sums, keys, B, W, M, tokens, parents, out_scores);
+  for (int32_t base = 0, n; base < B; base += n) {
+    n = std::min(B - base, kMaxGrid);
+    DSPARK_LAUNCH("beam_final", beam_final_kernel, dim3(static_cast<unsigned>(n)), dim3(kFinalThreads), 0, st, sums,
+                  keys, base, W, M, tokens, parents, out_scores);
+  }
   return hipGetLastError();
 }
 

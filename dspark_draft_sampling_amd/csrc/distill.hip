@@ -7,7 +7,7 @@
 //
 // Loss: a workgroup streams a draft row once and sums the mass of the tokens
 // outside the teacher's list, and of nothing else: the list becomes a bit mask in
-// LDS, one word per thread and group of 32 logits, so a group without a listed
+// LDS, one word per thread and group of 4 granules, so a group without a listed
 // token (nearly all) costs one LDS read and a branch.  Its first wave then forms
 // the K + 1 outcomes in 64 bits from that mass, the teacher's values and the
 // draft's logits at its tokens: where one probability is nearly 1, its logarithm
@@ -31,7 +31,8 @@
 namespace dspark {
 namespace {
 
-constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch; each then takes several items
+constexpr int kMaxGrid = 1 << 22;  // workgroups of a launch; more are further launches
+constexpr int kL = 4;              // granules of a group
 constexpr int kMaxTiles = 16;      // groups of a thread whose mask words are held at a time
 constexpr int kTinyThreads = 1024; // one-launch form: a wave a row
 constexpr int kTinyWaves = kTinyThreads / 64;
@@ -150,6 +151,7 @@ __device__ __forceinline__ Outcomes<ENT> outcomes(const Entries<ENT>& e, int K, 
   row_sync<64>();
   // entries of the same token
   int same[ENT] = {};
+#pragma unroll 4
   for (int j = 0; j < K; j += 4) {
     const int4 d = *reinterpret_cast<const int4*>(sh_ids + j);
 #pragma unroll
@@ -205,7 +207,7 @@ __device__ __forceinline__ Outcomes<ENT> outcomes(const Entries<ENT>& e, int K, 
 template <typename T, int NT, int TILES>
 __device__ __forceinline__ double outside_mass(const Row<T>& r, const DistillArgs& a, size_t row, int tid,
                                                uint32_t* member, Mass* shm) {
-  constexpr int EPL = Row<T>::EPL, L = group_granules<T>(), TILE = NT * L;
+  constexpr int EPL = Row<T>::EPL, L = kL, TILE = NT * L;
   const int groups = (r.Q + TILE - 1) / TILE;
   Mass acc = mass_none();
   uint4 u[L], w[L];
@@ -281,20 +283,17 @@ __device__ __forceinline__ float finish_row(const Entries<ENT>& e, const Distill
 
 // One workgroup a row.
 template <typename T, int NT, int ENT>
-__global__ __launch_bounds__(NT, 4) void distill_loss_kernel(const T* __restrict__ draft, DistillArgs a, int32_t R,
+__global__ __launch_bounds__(NT, 4) void distill_loss_kernel(const T* __restrict__ draft, DistillArgs a, int32_t base,
                                                              LossOut out) {
   __shared__ uint32_t member[kMaxTiles * NT];
   __shared__ __align__(16) int32_t sh_ids[64 * ENT];
   __shared__ Mass shm[NT / 64];
-  for (int rr = blockIdx.x; rr < R; rr += gridDim.x) {
-    const size_t row = static_cast<size_t>(rr);
-    const Row<T> r = make_row(draft + row * a.V, a.V);
-    Entries<ENT> e;
-    if (wave_id() == 0) e = load_entries<T, ENT>(r, a, row);  // on their way while the row streams
-    const double rest2 = outside_mass<T, NT, kMaxTiles>(r, a, row, threadIdx.x, member, shm);
-    if (wave_id() == 0) finish_row<ENT>(e, a, row, rest2, sh_ids, out);
-    __syncthreads();  // LDS is reused by the next row
-  }
+  const size_t row = static_cast<size_t>(base) + blockIdx.x;
+  const Row<T> r = make_row(draft + row * a.V, a.V);
+  Entries<ENT> e;
+  if (wave_id() == 0) e = load_entries<T, ENT>(r, a, row);  // on their way while the row streams
+  const double rest2 = outside_mass<T, NT, kMaxTiles>(r, a, row, threadIdx.x, member, shm);
+  if (wave_id() == 0) finish_row<ENT>(e, a, row, rest2, sh_ids, out);
 }
 
 // Row weights and sums.
@@ -435,116 +434,114 @@ __device__ __forceinline__ void gran_store(T* g, const Row<T>& r, int q, bool ve
 template <typename T, int NT, int ENT>
 __global__ __launch_bounds__(NT, 4) void distill_grad_kernel(const T* __restrict__ draft, DistillArgs a,
                                                              const float* __restrict__ rest,
-                                                             const float* __restrict__ grad_scale, int64_t items,
+                                                             const float* __restrict__ grad_scale, int64_t base,
                                                              int32_t P, int32_t groups, T* __restrict__ grad) {
-  constexpr int EPL = Row<T>::EPL, L = group_granules<T>(), TILE = NT * L;
+  constexpr int EPL = Row<T>::EPL, L = kL, TILE = NT * L;
   __shared__ __align__(16) int32_t sh_ids[64 * ENT];  // tokens to write over
   __shared__ float sh_d[64 * ENT];
   __shared__ double sh_t[64 * ENT];
   __shared__ float shc[2];  // factor, reference
   __shared__ int shf[2];    // a row of zeros; the reference is a logit
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const size_t row = static_cast<size_t>(item / P);
-    const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
-    const size_t b = row / a.gamma;
-    const Row<T> r = make_row(draft + row * a.V, a.V);
-    T* g = grad + row * a.V;
-    const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
-    const int first = seg * groups * TILE;
-    const int n = min(groups, (r.Q - first + TILE - 1) / TILE);
-    const bool live = !a.block_mask || a.block_mask[b] != 0;
-    uint4 ua[L], ub[L];
-    if (live && n > 0) group_load<T, NT, L>(r, first, tid, ua);
-    if (wave == 0) {
-      bool zero = true;
-      if (live) {
-        const float rst = rest[row];
-        const float scale = grad_scale ? grad_scale[0] : 1.0f;
-        const double rest2 = static_cast<double>(rst) * kLog2ed;
-        const Entries<ENT> e = load_entries<T, ENT>(r, a, row);
-        const Outcomes<ENT> o = outcomes<ENT>(e, a.K, rest2, a.c64, sh_ids);
-        const double w = static_cast<double>(scale) * a.weight * (a.c64 / kLog2ed) *
-                         exp(-static_cast<double>(row - b * a.gamma + 1) / a.gamma);
-        zero = o.empty && !o.bad;
-        double t[ENT];
+  const int64_t item = base + blockIdx.x;
+  const size_t row = static_cast<size_t>(item / P);
+  const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
+  const size_t b = row / a.gamma;
+  const Row<T> r = make_row(draft + row * a.V, a.V);
+  T* g = grad + row * a.V;
+  const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
+  const int first = seg * groups * TILE;
+  const int n = min(groups, (r.Q - first + TILE - 1) / TILE);
+  const bool live = !a.block_mask || a.block_mask[b] != 0;
+  uint4 ua[L], ub[L];
+  if (live && n > 0) group_load<T, NT, L>(r, first, tid, ua);
+  if (wave == 0) {
+    bool zero = true;
+    if (live) {
+      const float rst = rest[row];
+      const float scale = grad_scale ? grad_scale[0] : 1.0f;
+      const double rest2 = static_cast<double>(rst) * kLog2ed;
+      const Entries<ENT> e = load_entries<T, ENT>(r, a, row);
+      const Outcomes<ENT> o = outcomes<ENT>(e, a.K, rest2, a.c64, sh_ids);
+      const double w = static_cast<double>(scale) * a.weight * (a.c64 / kLog2ed) *
+                       exp(-static_cast<double>(row - b * a.gamma + 1) / a.gamma);
+      zero = o.empty && !o.bad;
+      double t[ENT];
 #pragma unroll
-        for (int i = 0; i < ENT; ++i) t[i] = e.id[i] >= 0 ? exp2(o.lt[i]) : 0.0;
-        if (o.twice) {
+      for (int i = 0; i < ENT; ++i) t[i] = e.id[i] >= 0 ? exp2(o.lt[i]) : 0.0;
+      if (o.twice) {
 #pragma unroll
-          for (int i = 0; i < ENT; ++i) sh_t[i * 64 + lane] = t[i];
-          row_sync<64>();
-#pragma unroll
-          for (int i = 0; i < ENT; ++i) {
-            t[i] = 0.0;
-            for (int j = 0; j < a.K; ++j) t[i] += sh_ids[j] == e.id[i] ? sh_t[j] : 0.0;
-          }
-          row_sync<64>();
-        }
-        const int32_t e0 = first * EPL - r.head, e1 = (first + groups * TILE) * EPL - r.head;  // of this segment
+        for (int i = 0; i < ENT; ++i) sh_t[i * 64 + lane] = t[i];
+        row_sync<64>();
 #pragma unroll
         for (int i = 0; i < ENT; ++i) {
-          sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls[i]) - t[i]));
-          sh_ids[i * 64 + lane] = ((o.first >> i) & 1u) && e.id[i] >= e0 && e.id[i] < e1 ? e.id[i] : -1;
+          t[i] = 0.0;
+          for (int j = 0; j < a.K; ++j) t[i] += sh_ids[j] == e.id[i] ? sh_t[j] : 0.0;
         }
-        if (lane == 0) {
-          // the reference is rounded to fp32; what that loses goes into the factor
-          float ref = static_cast<float>(rest2);
-          double lost = rest2 - static_cast<double>(ref);
-          const bool huge = fabsf(rst) >= kHugeLogit && rst != neg_inf();
-          if (huge) {  // x / T - rest is formed as (x - rest T) / T
-            ref = static_cast<float>(rest2 / a.c64);
-            lost = 0.0;
-          } else if (rst == neg_inf()) {  // no other token has mass
-            ref = 0.0f;
-            lost = 0.0;
-          }
-          shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls_r) - exp2(o.lt_r)) * exp2(-lost));
-          shc[1] = ref;
-          shf[1] = huge ? 1 : 0;
-        }
+        row_sync<64>();
       }
-      if (lane == 0) shf[0] = zero ? 1 : 0;
-    }
-    __syncthreads();
-    const float A = shc[0], ref = shc[1];
-    if (shf[0]) {
-      const float z[EPL] = {};
-      for (int t = 0; t < n; ++t)
+      const int32_t e0 = first * EPL - r.head, e1 = (first + groups * TILE) * EPL - r.head;  // of this segment
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int q = first + (t * L + i) * NT + tid;
-          if (q < r.Q) gran_store(g, r, q, vec, z);
-        }
-    } else {
-      const bool huge = shf[1] != 0;
-      auto put = [&](const uint4(&u)[L], int t) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int q = first + (t * L + i) * NT + tid;
-          float v[EPL];
-          if (huge) {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f((gran_elem(u[i], j, T{}) - ref) * a.c);
-          } else {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f(fmaf(gran_elem(u[i], j, T{}), a.c, -ref));
-          }
-          if (q < r.Q) gran_store(g, r, q, vec, v);
-        }
-      };
-      for (int t = 0; t < n; t += 2) {
-        if (t + 1 < n) group_load<T, NT, L>(r, first + (t + 1) * TILE, tid, ub);
-        put(ua, t);
-        if (t + 1 >= n) break;
-        if (t + 2 < n) group_load<T, NT, L>(r, first + (t + 2) * TILE, tid, ua);
-        put(ub, t + 1);
+      for (int i = 0; i < ENT; ++i) {
+        sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls[i]) - t[i]));
+        sh_ids[i * 64 + lane] = ((o.first >> i) & 1u) && e.id[i] >= e0 && e.id[i] < e1 ? e.id[i] : -1;
       }
-      __syncthreads();  // the listed tokens are written after the granules that hold them
-      for (int j = tid; j < a.K; j += NT)
-        if (sh_ids[j] >= 0) store_elem(g + sh_ids[j], sh_d[j]);
+      if (lane == 0) {
+        // the reference is rounded to fp32; what that loses goes into the factor
+        float ref = static_cast<float>(rest2);
+        double lost = rest2 - static_cast<double>(ref);
+        const bool huge = fabsf(rst) >= kHugeLogit && rst != neg_inf();
+        if (huge) {  // x / T - rest is formed as (x - rest T) / T
+          ref = static_cast<float>(rest2 / a.c64);
+          lost = 0.0;
+        } else if (rst == neg_inf()) {  // no other token has mass
+          ref = 0.0f;
+          lost = 0.0;
+        }
+        shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls_r) - exp2(o.lt_r)) * exp2(-lost));
+        shc[1] = ref;
+        shf[1] = huge ? 1 : 0;
+      }
     }
-    __syncthreads();  // LDS is reused by the next item
+    if (lane == 0) shf[0] = zero ? 1 : 0;
+  }
+  __syncthreads();
+  const float A = shc[0], ref = shc[1];
+  if (shf[0]) {
+    const float z[EPL] = {};
+    for (int t = 0; t < n; ++t)
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int q = first + (t * L + i) * NT + tid;
+        if (q < r.Q) gran_store(g, r, q, vec, z);
+      }
+  } else {
+    const bool huge = shf[1] != 0;
+    auto put = [&](const uint4(&u)[L], int t) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int q = first + (t * L + i) * NT + tid;
+        float v[EPL];
+        if (huge) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f((gran_elem(u[i], j, T{}) - ref) * a.c);
+        } else {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) v[j] = A * __builtin_amdgcn_exp2f(fmaf(gran_elem(u[i], j, T{}), a.c, -ref));
+        }
+        if (q < r.Q) gran_store(g, r, q, vec, v);
+      }
+    };
+    for (int t = 0; t < n; t += 2) {
+      if (t + 1 < n) group_load<T, NT, L>(r, first + (t + 1) * TILE, tid, ub);
+      put(ua, t);
+      if (t + 1 >= n) break;
+      if (t + 2 < n) group_load<T, NT, L>(r, first + (t + 2) * TILE, tid, ua);
+      put(ub, t + 1);
+    }
+    __syncthreads();  // the listed tokens are written after the granules that hold them
+    for (int j = tid; j < a.K; j += NT)
+      if (sh_ids[j] >= 0) store_elem(g + sh_ids[j], sh_d[j]);
   }
 }
 
@@ -554,20 +551,23 @@ int row_granules(int epl, int32_t V) { return static_cast<int>((static_cast<int6
 template <typename T, int ENT>
 hipError_t launch_loss(const T* draft, const DistillArgs& a, int32_t R, const LossOut& out, float* sums, Sums* partial,
                        hipStream_t st) {
-  constexpr int L = group_granules<T>();
+  constexpr int L = kL;
   const int q = row_granules(Row<T>::EPL, a.V);
   if (R <= 64 && q <= kTinyTiles * 64 * L) {
     DSPARK_LAUNCH("distill_tiny", (distill_tiny_kernel<T, ENT>), dim3(1), dim3(kTinyThreads), 0, st, draft, a, R, out,
                   sums);
     return hipGetLastError();
   }
-  const dim3 grid(static_cast<unsigned>(std::min(R, kMaxGrid)));
-  if (q <= 2 * 64 * L)
-    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, R, out);
-  else if (R > 512 || q <= 4 * 256 * L)
-    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, R, out);
-  else
-    DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 512, ENT>), grid, dim3(512), 0, st, draft, a, R, out);
+  for (int32_t base = 0, n; base < R; base += n) {
+    n = std::min(R - base, kMaxGrid);
+    const dim3 grid(static_cast<unsigned>(n));
+    if (q <= 2 * 64 * L)
+      DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, base, out);
+    else if (R > 512 || q <= 4 * 256 * L)
+      DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, base, out);
+    else
+      DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 512, ENT>), grid, dim3(512), 0, st, draft, a, base, out);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int blocks = std::min(kMaxSumBlocks, (R + 16383) / 16384);
@@ -582,21 +582,23 @@ hipError_t launch_loss(const T* draft, const DistillArgs& a, int32_t R, const Lo
 template <typename T, int ENT>
 hipError_t launch_grad(const T* draft, const DistillArgs& a, int32_t R, const float* rest, const float* grad_scale,
                        T* grad, hipStream_t st) {
-  constexpr int L = group_granules<T>();
+  constexpr int L = kL;
   const int q = row_granules(Row<T>::EPL, a.V);
   const int nt = q <= 2 * 64 * L ? 64 : 256;
   const int need = (q + nt * L - 1) / (nt * L);  // groups of a thread over the row
   int groups = need;  // shorter segments where that fills the GPU
-  while (groups > 1 && static_cast<int64_t>(R) * ((need + groups - 1) / groups) < 1024) groups = (groups + 1) / 2;
+  while (groups > 1 && static_cast<int64_t>(R) * ((need + groups - 1) / groups) < 512) groups = (groups + 1) / 2;
   const int P = (need + groups - 1) / groups;
   const int64_t items = static_cast<int64_t>(R) * P;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid)));
-  if (nt == 64)
-    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, rest, grad_scale,
-                  items, P, groups, grad);
-  else
-    DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, rest,
-                  grad_scale, items, P, groups, grad);
+  for (int64_t base = 0; base < items; base += kMaxGrid) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));
+    if (nt == 64)
+      DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, rest,
+                    grad_scale, base, P, groups, grad);
+    else
+      DSPARK_LAUNCH("distill_grad", (distill_grad_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, rest,
+                    grad_scale, base, P, groups, grad);
+  }
   return hipGetLastError();
 }
 

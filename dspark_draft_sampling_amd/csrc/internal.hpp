@@ -159,10 +159,10 @@ struct Mass;  // rowstream.hpp
 float mass_scale(float temperature);
 double mass_scale64(float temperature);
 
-// How a row is cut: P segments of `groups` groups a thread, workgroups of NT
-// threads; groups = 0: short rows, NT granules a lane of one wave.
+// How a row is cut: P segments of `groups` groups of L granules a thread,
+// workgroups of NT threads; groups = 0: short rows, NT granules a lane of one wave.
 struct TopSplit {
-  int NT, groups, P;
+  int NT, L, groups, P;
 };
 struct TopPlan {
   int P;  // most segments of a row

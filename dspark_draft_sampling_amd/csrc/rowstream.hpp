@@ -45,12 +45,10 @@ __device__ __forceinline__ float gran_elem(const uint4& u, int j, float) {
   return __uint_as_float(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
 }
 
-// Granule q, elements outside the row as -inf.
+// A granule with elements of the row and others: element by element, the others
+// as -inf.  A row has two of them at most.
 template <typename T>
-__device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
-  constexpr int EPL = Row<T>::EPL;
-  const int e0 = q * EPL - r.head;
-  if (e0 >= 0 && e0 + EPL <= r.V) return *reinterpret_cast<const uint4*>(r.p + e0);
+__device__ __forceinline__ uint4 gran_partial(const Row<T>& r, int e0) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -67,6 +65,15 @@ __device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Granule q, elements outside the row as -inf.
+template <typename T>
+__device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
+  constexpr int EPL = Row<T>::EPL;
+  const int e0 = q * EPL - r.head;
+  if (e0 >= 0 && e0 + EPL <= r.V) return *reinterpret_cast<const uint4*>(r.p + e0);
+  return gran_partial(r, e0);
+}
+
 // Keeps the compiler from holding a granule's unpacked elements in registers
 // from one pass over them to the next (they are one instruction away).
 __device__ __forceinline__ void repack(uint4& u) { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }
@@ -81,15 +88,26 @@ __device__ __forceinline__ void group_load(const Row<T>& r, int q0, int tid, uin
 #pragma unroll
     for (int i = 0; i < L; ++i) u[i] = *reinterpret_cast<const uint4*>(p + i * NT * EPL);
   } else {
+    // the whole granules first, all in flight together; others read the row's
+    // first whole granule in their place
+    constexpr uint32_t kNeg = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    const int whole = r.head ? EPL - r.head : 0;
+    if (whole + EPL <= r.V) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) u[i] = gran_load(r, q0 + i * NT + tid);
+      for (int i = 0; i < L; ++i) {
+        const int e0 = (q0 + i * NT + tid) * EPL - r.head;
+        u[i] = *reinterpret_cast<const uint4*>(r.p + (e0 >= 0 && e0 + EPL <= r.V ? e0 : whole));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int e0 = (q0 + i * NT + tid) * EPL - r.head;
+      if (e0 < 0 || e0 + EPL > r.V) {
+        u[i] = make_uint4(kNeg, kNeg, kNeg, kNeg);
+        if (e0 + EPL > 0 && e0 < r.V) u[i] = gran_partial(r, e0);
+      }
+    }
   }
-}
-
-// Granules of a group: 32 logits.
-template <typename T>
-constexpr int group_granules() {
-  return sizeof(T) == 2 ? 4 : 8;
 }
 
 // ---- masses ----------------------------------------------------------------------
@@ -258,31 +276,26 @@ __device__ __forceinline__ int block_scan(int v, int* slots, int& total) {
   }
 }
 
-// Three per-wave counts summed over the workgroup, on every thread.  slots: 6
-// NW ints, used in turn by `step`, so that one barrier a call is enough.
+// Three per-wave counts (under 2^21 in total) summed over the workgroup, on every
+// thread.  slots: 2 NW words, used in turn by `step`, so that one barrier a call
+// is enough.
 struct Count3 {
   int a, b, c;
 };
 template <int NW>
-__device__ __forceinline__ Count3 block_count(Count3 n, int* slots, int& step) {
+__device__ __forceinline__ Count3 block_count(Count3 n, uint64_t* slots, int& step) {
   if constexpr (NW == 1) {
     return n;
   } else {
-    int* s = slots + (step++ & 1) * 3 * NW;
-    if ((threadIdx.x & 63) == 0) {
-      s[threadIdx.x >> 6] = n.a;
-      s[NW + (threadIdx.x >> 6)] = n.b;
-      s[2 * NW + (threadIdx.x >> 6)] = n.c;
-    }
+    uint64_t* s = slots + (step++ & 1) * NW;
+    if ((threadIdx.x & 63) == 0)
+      s[threadIdx.x >> 6] = static_cast<uint64_t>(n.a) | static_cast<uint64_t>(n.b) << 21 | static_cast<uint64_t>(n.c) << 42;
     __syncthreads();
-    Count3 t{0, 0, 0};
+    uint64_t t = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      t.a += s[w];
-      t.b += s[NW + w];
-      t.c += s[2 * NW + w];
-    }
-    return t;
+    for (int w = 0; w < NW; ++w) t += s[w];
+    constexpr uint64_t m = (1u << 21) - 1;
+    return Count3{static_cast<int>(t & m), static_cast<int>(t >> 21 & m), static_cast<int>(t >> 42)};
   }
 }
 

@@ -5,7 +5,7 @@
 // natural logarithm of sum exp(x / T) over the other tokens and over all.
 //
 // One pass over the row.  A workgroup takes a segment of a row, every thread
-// up to 16 groups of 32 logits, and keeps of each
+// up to 16 groups of 4 granules, and keeps of each
 // group its maximum and its mass (rowstream.hpp) in LDS: one exponential and
 // about 7.5 VALU slots per element, no running maximum and no candidate test in
 // the stream.  K or a few more of the threads' maxima (of the groups' where K
@@ -36,14 +36,14 @@ namespace dspark {
 namespace {
 
 constexpr int kMergeThreads = 256;
-constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch; each then takes several items
+constexpr int kMaxGrid = 1 << 22;  // workgroups of a launch; more are further launches
 
 // Groups of a thread at most (they are kept in LDS) and keys that are ranked at
 // once: more are first cut by a search.
 template <int NT>
 struct TopCaps {
   static constexpr int kG = NT == 512 ? 8 : 16;
-  static constexpr int kRank = NT == 64 ? 128 : 512;
+  static constexpr int kRank = NT == 64 ? 448 : 512;
 };
 
 // Candidates a list may hold beyond K: the searches stop at the first bound
@@ -100,7 +100,7 @@ __device__ __forceinline__ bool unread_beam(const TopBeams& bm, const TopOut& o,
 // there are no more.  found: the number of keys that are not 0.
 template <int NT>
 __device__ __forceinline__ uint64_t list_bound(const uint64_t* cand, int n, int found, int K, uint64_t lo, uint64_t hi,
-                                               int* slots, int& step) {
+                                               uint64_t* slots, int& step) {
   constexpr int NW = NT / 64;
   if (found <= list_len(K)) return lo;
   const int n64 = (n + 63) / 64 * 64;
@@ -116,70 +116,107 @@ __device__ __forceinline__ uint64_t list_bound(const uint64_t* cand, int n, int 
   });
 }
 
-// The K best of n distinct keys in LDS in descending order into sorted[0, K) (0
-// where there are fewer), each at its rank, the number of greater keys.  keys
-// has room for 4 more; 0s among them are none.  Complete on return.
 template <int NT>
-__device__ __forceinline__ void rank_keys(uint64_t* keys, int n, int K, uint64_t* sorted) {
-  const int tid = threadIdx.x;
-  for (int j = tid; j < K; j += NT) sorted[j] = 0;
-  if (tid < 4) keys[n + tid] = 0;
+struct RankLds {
+  uint16_t rank[TopCaps<NT>::kRank];
+  Mass others[NT / 64], top[NT / 64];
+  double sum[NT / 64];
+};
+
+// Outputs of a row or beam from its n candidates in LDS (distinct keys, 0s
+// among them are none, room for 4 more; nv of them are not 0) and the threads'
+// shares of the mass of all other elements.  A candidate's rank is the number of
+// greater keys; those below K are the outputs, the others' mass joins the rest.
+// wmax: the row's largest value.  bad, or a NaN mass: a NaN or +inf was seen.
+// A beam's normaliser is formed in 64 bits, its K best tokens one by one.
+template <int NT, TopMode MODE>
+__device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K, Mass others, bool bad, float wmax,
+                                           size_t row, float c, double c64, const TopBeams& bm, const TopOut& o,
+                                           RankLds<NT>& s) {
+  constexpr int NW = NT / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  if (tid < 4) list[n + tid] = 0;
   __syncthreads();
+  Mass top = mass_none();
+  double sum = 0.0;
   for (int i = tid; i < n; i += NT) {
-    const uint64_t k = keys[i];
-    if (k == 0) continue;
+    const uint64_t k = list[i];
     int rank = 0;
+#pragma unroll 2
     for (int j = 0; j < n; j += 4) {
-      const uint64_t k0 = keys[j], k1 = keys[j + 1], k2 = keys[j + 2], k3 = keys[j + 3];
+      const uint64_t k0 = list[j], k1 = list[j + 1], k2 = list[j + 2], k3 = list[j + 3];
       rank += (k0 > k) + (k1 > k) + (k2 > k) + (k3 > k);
     }
-    if (rank < K) sorted[rank] = k;
+    if (MODE == kBeams) s.rank[i] = static_cast<uint16_t>(rank);
+    if (k == 0) continue;
+    const float x = key_value(k);
+    if (rank >= K) {
+      others = mass_add(others, Mass{x, 1.0f}, c);
+    } else if constexpr (MODE == kRows) {
+      o.values[row * K + rank] = x;
+      o.ids[row * K + rank] = key_index(k);
+      top = mass_add(top, Mass{x, 1.0f}, c);
+    } else {
+      sum += exp2((static_cast<double>(x) - static_cast<double>(wmax)) * c64);
+    }
   }
-  __syncthreads();
-}
-
-// A row's outputs from its sorted keys and the mass of the others (by the
-// first wave; `others` valid on its lanes, bad: a NaN or +inf was seen).
-__device__ __forceinline__ void write_row(const TopOut& o, size_t row, const uint64_t* sorted, int K, Mass others,
-                                          bool bad, float c, double c64) {
-  const int lane = threadIdx.x;
-  Mass top = mass_none();
-  for (int j = lane; j < K; j += 64) {
-    const uint64_t k = bad ? 0 : sorted[j];
-    const float x = k ? key_value(k) : neg_inf();
-    o.values[row * K + j] = x;
-    o.ids[row * K + j] = k ? key_index(k) : -1;
-    if (k) top = mass_add(top, Mass{x, 1.0f}, c);
+  others = wave_mass(others, c);
+  if constexpr (MODE == kRows)
+    top = wave_mass(top, c);
+  else
+    sum = wave_sum64(sum);
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+      s.others[wave] = others;
+      if constexpr (MODE == kRows)
+        s.top[wave] = top;
+      else
+        s.sum[wave] = sum;
+    }
+    __syncthreads();
+    others = wave_mass(lane < NW ? s.others[lane] : mass_none(), c);
+    if constexpr (MODE == kRows) {
+      top = wave_mass(lane < NW ? s.top[lane] : mass_none(), c);
+    } else {
+      sum = 0.0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) sum += s.sum[w];
+    }
   }
-  top = wave_mass(top, c);
-  if (lane == 0) {
-    const double r = mass_log2(others, c, c64);
-    const double l = log2_add(r, mass_log2(top, c, c64));
-    const float nan = __builtin_nanf("");
-    o.rest[row] = bad ? nan : static_cast<float>(r * 0.69314718055994530942);
-    o.lse[row] = bad ? nan : static_cast<float>(l * 0.69314718055994530942);
-    o.flags[row] = bad ? DSPARK_FLAG_NONFINITE : l == -__builtin_inf() ? DSPARK_FLAG_EMPTY_ROW : 0;
+  bad |= !(others.s >= 0.0f);
+  if (bad) nv = 0;
+  if constexpr (MODE == kRows) {
+    if (bad) __syncthreads();  // its candidates have been written: now none are there
+    for (int j = nv + tid; j < K; j += NT) {
+      o.values[row * K + j] = neg_inf();
+      o.ids[row * K + j] = -1;
+    }
+    if (tid == 0) {
+      const double r = mass_log2(others, c, c64);
+      const double l = log2_add(r, mass_log2(top, c, c64));
+      const float nan = __builtin_nanf("");
+      o.rest[row] = bad ? nan : static_cast<float>(r * 0.69314718055994530942);
+      o.lse[row] = bad ? nan : static_cast<float>(l * 0.69314718055994530942);
+      o.flags[row] = bad ? DSPARK_FLAG_NONFINITE : l == -__builtin_inf() ? DSPARK_FLAG_EMPTY_ROW : 0;
+    }
+  } else {
+    const double ref = static_cast<double>(wmax);
+    const double lse = ref + log2(sum + exp2(mass_log2(others, c, c64) - ref * c64)) / c64;
+    const double sc = static_cast<double>(bm.scores[row]);
+    if (!bad)
+      for (int i = tid; i < n; i += NT) {
+        const int rank = s.rank[i];
+        const uint64_t k = list[i];
+        if (k == 0 || rank >= K) continue;
+        bm.sums[row * K + rank] = order_key(sc + (static_cast<double>(key_value(k)) - lse));
+        o.keys[row * K + rank] = k;
+      }
+    for (int j = nv + tid; j < K; j += NT) {
+      bm.sums[row * K + j] = kKey64NegInf;
+      o.keys[row * K + j] = 0;
+    }
+    if (tid == 0) bm.flags[row] = bad ? DSPARK_FLAG_NONFINITE : nv == 0 ? DSPARK_FLAG_EMPTY_ROW : 0;
   }
-}
-
-// A beam's candidates from its sorted keys and the mass of its other tokens (by
-// the first wave): the normaliser in 64 bits, the listed tokens one by one.
-__device__ __forceinline__ void write_beam(const TopBeams& bm, const TopOut& o, size_t row, const uint64_t* sorted,
-                                           int K, Mass others, bool bad, float c, double c64) {
-  const int lane = threadIdx.x;
-  const uint64_t best = bad ? 0 : sorted[0];
-  const double ref = best ? static_cast<double>(key_value(best)) : 0.0;
-  double sum = 0.0;
-  for (int j = lane; j < K; j += 64)
-    if (sorted[j]) sum += exp2((static_cast<double>(key_value(sorted[j])) - ref) * c64);
-  sum = wave_sum64(sum) + exp2(mass_log2(others, c, c64) - ref * c64);
-  const double lse = ref + log2(sum) / c64, sc = static_cast<double>(bm.scores[row]);
-  for (int j = lane; j < K; j += 64) {
-    const uint64_t k = bad ? 0 : sorted[j];
-    bm.sums[row * K + j] = k ? order_key(sc + (static_cast<double>(key_value(k)) - lse)) : kKey64NegInf;
-    o.keys[row * K + j] = k;
-  }
-  if (lane == 0) bm.flags[row] = bad ? DSPARK_FLAG_NONFINITE : best == 0 ? DSPARK_FLAG_EMPTY_ROW : 0;
 }
 
 // Mass of a granule's elements for which keep(value, index) holds.
@@ -208,12 +245,12 @@ struct TopLds {
     uint64_t cand[kCand + 4];  // then the candidates
   };
   uint64_t list[kMaxList + 4];
-  uint64_t sorted[DSPARK_MAX_TOP];
   uint16_t qual[NT == 64 ? 256 : 512];  // groups read again
-  int slots[6 * (NT / 64)];
+  uint64_t slots[2 * (NT / 64)];
   int scan[2][NT / 64];
   float red[3][NT / 64];
   Mass mass[NT / 64];
+  RankLds<NT> out;
 };
 
 // Candidates of a segment by a search over its elements (rows where the bound
@@ -221,7 +258,7 @@ struct TopLds {
 // the mass of all other elements as each thread's share.  scan: NW ints.
 template <typename T, int NT>
 __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1, int K, uint32_t kmax, float c,
-                                                uint64_t* cand, int* slots, int* scan, int& step, Mass& others) {
+                                                uint64_t* cand, uint64_t* slots, int* scan, int& step, Mass& others) {
   constexpr int NW = NT / 64;
   constexpr int EPL = Row<T>::EPL;
   const int tid = threadIdx.x;
@@ -295,214 +332,202 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
   return total;
 }
 
-template <typename T, int NT, TopMode MODE>
-__global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict__ logits, int64_t items, int32_t V,
+template <typename T, int NT, int kL, TopMode MODE>
+__global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict__ logits, int64_t base, int32_t V,
                                                             int32_t K, int32_t P, int32_t groups, float c, double c64,
                                                             TopBeams bm, TopOut o) {
   constexpr int NW = NT / 64;
-  constexpr int EPL = Row<T>::EPL, kL = group_granules<T>();
+  constexpr int EPL = Row<T>::EPL, G = TopCaps<NT>::kG;
   constexpr int TILE = NT * kL;  // granules of a group over the workgroup
   __shared__ TopLds<NT> s;
   constexpr int QUAL = sizeof(s.qual) / sizeof(uint16_t), CAND = TopLds<NT>::kCand;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   int step = 0;
 
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const size_t row = static_cast<size_t>(item / P);
-    const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
-    if (unread_beam<NT, MODE>(bm, o, row, K)) continue;
-    const Row<T> r = make_row(logits + row * V, V);
-    const int first = seg * groups * TILE;
-    const int n = min(groups, (r.Q - first + TILE - 1) / TILE);  // <= 0: nothing left of this row
+  const int64_t item = base + blockIdx.x;
+  const size_t row = static_cast<size_t>(item / P);
+  const int seg = static_cast<int>(item - static_cast<int64_t>(row) * P);
+  if (unread_beam<NT, MODE>(bm, o, row, K)) return;
+  const Row<T> r = make_row(logits + row * V, V);
+  const int first = seg * groups * TILE;
+  const int n = min(groups, (r.Q - first + TILE - 1) / TILE);  // <= 0: nothing left of this row
 
-    // ---- stream: every group's maximum and mass ----
-    float lmax = neg_inf();
-    bool bad = false;
-    {
-      uint4 a[kL], b[kL];
-      auto take = [&](const uint4(&u)[kL], int g) {
-        const Mass m = group_mass<T, kL>(u, c);
-        s.grp[g * NT + tid] = m;
-        lmax = fmaxf(lmax, m.m);
-        bad |= !(m.s >= 0.0f);
-      };
-      if (n > 0) group_load<T, NT, kL>(r, first, tid, a);
-      for (int g = 0; g < n; g += 2) {
-        if (g + 1 < n) group_load<T, NT, kL>(r, first + (g + 1) * TILE, tid, b);
-        take(a, g);
-        if (g + 1 >= n) break;
-        if (g + 2 < n) group_load<T, NT, kL>(r, first + (g + 2) * TILE, tid, a);
-        take(b, g + 1);
-      }
+  // ---- stream: every group's maximum and mass ----
+  float lmax = neg_inf();
+  bool bad = false;
+  {
+    uint4 a[kL], b[kL];
+    auto take = [&](const uint4(&u)[kL], int g) {
+      const Mass m = group_mass<T, kL>(u, c);
+      s.grp[g * NT + tid] = m;
+      lmax = fmaxf(lmax, m.m);
+      bad |= !(m.s >= 0.0f);
+    };
+    if (n > 0) group_load<T, NT, kL>(r, first, tid, a);
+    for (int g = 0; g < n; g += 2) {
+      if (g + 1 < n) group_load<T, NT, kL>(r, first + (g + 1) * TILE, tid, b);
+      take(a, g);
+      if (g + 1 >= n) break;
+      if (g + 2 < n) group_load<T, NT, kL>(r, first + (g + 2) * TILE, tid, a);
+      take(b, g + 1);
     }
+  }
 
-    // ---- range of the maxima, bad values ----
-    float wmax = wave_max(lmax), wmin = -wave_max(-lmax);
-    bad = __any(bad);
-    if constexpr (NW > 1) {
-      if (lane == 0) {
-        s.red[0][wave] = wmax;
-        s.red[1][wave] = wmin;
-        s.red[2][wave] = bad ? 1.0f : 0.0f;
-      }
-      __syncthreads();
+  // ---- range of the maxima, bad values ----
+  float wmax = wave_max(lmax), wmin = -wave_max(-lmax);
+  bad = __any(bad);
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+      s.red[0][wave] = wmax;
+      s.red[1][wave] = wmin;
+      s.red[2][wave] = bad ? 1.0f : 0.0f;
+    }
+    __syncthreads();
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        wmax = fmaxf(wmax, s.red[0][w]);
-        wmin = fminf(wmin, s.red[1][w]);
-        bad |= s.red[2][w] != 0.0f;
-      }
+    for (int w = 0; w < NW; ++w) {
+      wmax = fmaxf(wmax, s.red[0][w]);
+      wmin = fminf(wmin, s.red[1][w]);
+      bad |= s.red[2][w] != 0.0f;
     }
+  }
 
-    Mass others = mass_none();
-    int nl = 0;  // candidates listed
-    uint64_t* list = s.cand;
-    if (!bad && wmax > neg_inf()) {
-      // ---- bound: at least K threads' (or groups') maxima reach it, or all finite ones ----
-      const uint32_t kmax = order_key(wmax);
-      uint32_t bound = kKeyNegInf + 1;
-      if (K <= NT / 2) {
-        const uint32_t k = order_key(lmax);
-        int nb = wmin > neg_inf() ? NT : INT32_MAX;
-        if (wmin > neg_inf()) {
-          bound = order_key(wmin);
-        } else {
-          const int w = __popcll(__ballot(k >= bound));
-          nb = block_count<NW>(Count3{w, 0, 0}, s.slots, step).a;
-        }
-        if (nb > K)
-          bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-            return block_count<NW>(Count3{static_cast<int>(__popcll(__ballot(k >= t1))), static_cast<int>(__popcll(__ballot(k >= t2))),
-                                          static_cast<int>(__popcll(__ballot(k >= t3)))}, s.slots, step);
-          });
+  Mass others = mass_none();
+  int nl = 0;  // candidates listed
+  uint64_t* list = s.cand;
+  if (!bad && wmax > neg_inf()) {
+    // ---- bound: at least K threads' (or groups') maxima reach it, or all finite ones ----
+    const uint32_t kmax = order_key(wmax);
+    uint32_t bound = kKeyNegInf + 1;
+    if (K <= NT / 2) {
+      const uint32_t k = order_key(lmax);
+      int nb = wmin > neg_inf() ? NT : INT32_MAX;
+      if (wmin > neg_inf()) {
+        bound = order_key(wmin);
       } else {
-        auto groups_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-          Count3 w{0, 0, 0};
-          for (int g = 0; g < n; ++g) {
-            const uint32_t k = order_key(s.grp[g * NT + tid].m);
-            w.a += __popcll(__ballot(k >= t1));
-            w.b += __popcll(__ballot(k >= t2));
-            w.c += __popcll(__ballot(k >= t3));
-          }
-          return block_count<NW>(w, s.slots, step);
-        };
-        int nb = groups_at(bound, bound, bound).a;
-        if (nb > K) bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), groups_at);
+        const int w = __popcll(__ballot(k >= bound));
+        nb = block_count<NW>(Count3{w, 0, 0}, s.slots, step).a;
       }
-      const float at = key_value(bound);
-
-      // ---- the groups at the bound, in thread order; the mass of the others ----
-      int mine = 0;
-      float om = neg_inf(), os = 0.0f;
-      for (int g = 0; g < n; ++g) {
-        const float m = s.grp[g * NT + tid].m;
-        if (m >= at) {
-          ++mine;
-        } else {
-          om = fmaxf(om, m);
+      if (nb > K)
+        bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+          return block_count<NW>(Count3{static_cast<int>(__popcll(__ballot(k >= t1))), static_cast<int>(__popcll(__ballot(k >= t2))),
+                                        static_cast<int>(__popcll(__ballot(k >= t3)))}, s.slots, step);
+        });
+    } else {
+      auto groups_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+        Count3 w{0, 0, 0};
+        for (int g = 0; g < n; ++g) {
+          const uint32_t k = order_key(s.grp[g * NT + tid].m);
+          w.a += __popcll(__ballot(k >= t1));
+          w.b += __popcll(__ballot(k >= t2));
+          w.c += __popcll(__ballot(k >= t3));
         }
-      }
-      int nq;
-      int pos = block_scan<NW>(mine, s.scan[0], nq);
-      const bool fits = nq <= QUAL;
-      for (int g = 0; g < n; ++g) {
-        const Mass m = s.grp[g * NT + tid];
-        if (m.m >= at) {
-          if (fits) s.qual[pos++] = static_cast<uint16_t>(g * NT + tid);
-        } else if (m.m > neg_inf()) {
-          os += m.s * __builtin_amdgcn_exp2f(mass_gap(m.m, om, c));
-        }
-      }
-      others = Mass{om, os};
-      __syncthreads();
+        return block_count<NW>(w, s.slots, step);
+      };
+      int nb = groups_at(bound, bound, bound).a;
+      if (nb > K) bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), groups_at);
+    }
+    const float at = key_value(bound);
 
-      // ---- candidates: their elements at or above the bound, in thread order ----
-      const int q1 = min(r.Q, first + n * TILE);
-      int nc = CAND + 1;
-      if (fits) {
-        auto granule = [&](int i) {  // i-th granule read again
-          const int g = s.qual[i / kL];
-          return first + (g / NT * kL + i % kL) * NT + g % NT;
-        };
-        mine = 0;
-        uint4 mineu = make_uint4(0, 0, 0, 0);  // the thread's first granule
+    // ---- the groups at the bound, in thread order; the mass of the others ----
+    Mass m[G];  // all of them at once, so that the reads overlap
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      m[g] = s.grp[min(g, n - 1) * NT + tid];
+      if (g >= n) m[g] = mass_none();
+    }
+    int mine = 0;
+    float om = neg_inf(), os = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      mine += m[g].m >= at;
+      om = fmaxf(om, m[g].m >= at ? neg_inf() : m[g].m);
+    }
+    int nq;
+    int pos = block_scan<NW>(mine, s.scan[0], nq);
+    const bool fits = nq <= QUAL;
+    if (mine > 0 && fits) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (m[g].m >= at) s.qual[pos++] = static_cast<uint16_t>(g * NT + tid);
+    }
+    if (om > neg_inf()) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        os += (m[g].m >= at ? 0.0f : m[g].s) * __builtin_amdgcn_exp2f(fminf(mass_gap(m[g].m, om, c), 0.0f));
+    }
+    others = Mass{om, os};
+    __syncthreads();
+
+    // ---- candidates: their elements at or above the bound, in thread order ----
+    const int q1 = min(r.Q, first + n * TILE);
+    int nc = CAND + 1;
+    if (fits) {
+      auto granule = [&](int i) {  // i-th granule read again
+        const int g = s.qual[i / kL];
+        return first + (g / NT * kL + i % kL) * NT + g % NT;
+      };
+      mine = 0;
+      uint4 mineu = make_uint4(0, 0, 0, 0);  // the thread's first granule
+      for (int i = tid; i < nq * kL; i += NT) {
+        const int q = granule(i);
+        if (q >= q1) continue;
+        const uint4 u = gran_load(r, q);
+        if (i == tid) mineu = u;
+        others = mass_add(others, gran_mass<T>(u, 0, c, [&](float x, int) {
+          mine += x >= at;
+          return !(x >= at);
+        }), c);
+      }
+      pos = block_scan<NW>(mine, s.scan[1], nc);
+      if (nc <= CAND && mine > 0) {
         for (int i = tid; i < nq * kL; i += NT) {
           const int q = granule(i);
           if (q >= q1) continue;
-          const uint4 u = gran_load(r, q);
-          if (i == tid) mineu = u;
-          others = mass_add(others, gran_mass<T>(u, 0, c, [&](float x, int) {
-            mine += x >= at;
-            return !(x >= at);
-          }), c);
-        }
-        pos = block_scan<NW>(mine, s.scan[1], nc);
-        if (nc <= CAND && mine > 0) {
-          for (int i = tid; i < nq * kL; i += NT) {
-            const int q = granule(i);
-            if (q >= q1) continue;
-            const uint4 u = i == tid ? mineu : gran_load(r, q);
+          const uint4 u = i == tid ? mineu : gran_load(r, q);
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-              const float x = gran_elem(u, j, T{});
-              if (x >= at) s.cand[pos++] = cand_key(order_key(x), q * EPL - r.head + j);
-            }
+          for (int j = 0; j < EPL; ++j) {
+            const float x = gran_elem(u, j, T{});
+            if (x >= at) s.cand[pos++] = cand_key(order_key(x), q * EPL - r.head + j);
           }
         }
-        __syncthreads();
       }
-      if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s.cand, s.slots, s.scan[0], step, others);
+      __syncthreads();
+    }
+    if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s.cand, s.slots, s.scan[0], step, others);
 
-      // ---- the K best of them or a few more; the others' mass ----
-      nl = nc;
-      if (nc > (MODE == kLists ? list_len(K) : TopCaps<NT>::kRank)) {
-        const uint64_t t = list_bound<NT>(s.cand, nc, nc, K, static_cast<uint64_t>(bound) << 32,
-                                          static_cast<uint64_t>(kmax + 1) << 32, s.slots, step);
-        mine = 0;
-        for (int i = tid; i < nc; i += NT) mine += s.cand[i] >= t;
-        pos = block_scan<NW>(mine, s.scan[0], nl);
-        for (int i = tid; i < nc; i += NT) {
-          const uint64_t k = s.cand[i];
-          if (k >= t) {
-            s.list[pos++] = k;
-          } else {
-            others = mass_add(others, Mass{key_value(k), 1.0f}, c);
-          }
+    // ---- the K best of them or a few more; the others' mass ----
+    nl = nc;
+    if (nc > (MODE == kLists ? list_len(K) : NT == 64 ? 2 * list_len(K) : TopCaps<NT>::kRank)) {
+      const uint64_t t = list_bound<NT>(s.cand, nc, nc, K, static_cast<uint64_t>(bound) << 32,
+                                        static_cast<uint64_t>(kmax + 1) << 32, s.slots, step);
+      mine = 0;
+      for (int i = tid; i < nc; i += NT) mine += s.cand[i] >= t;
+      pos = block_scan<NW>(mine, s.scan[0], nl);
+      for (int i = tid; i < nc; i += NT) {
+        const uint64_t k = s.cand[i];
+        if (k >= t) {
+          s.list[pos++] = k;
+        } else {
+          others = mass_add(others, Mass{key_value(k), 1.0f}, c);
         }
-        __syncthreads();
-        list = s.list;
       }
-      if constexpr (MODE != kLists) {
-        rank_keys<NT>(list, nl, K, s.sorted);
-        const uint64_t kth = s.sorted[K - 1];  // 0: fewer than K, all of them are in
-        for (int i = tid; i < nl; i += NT)
-          if (list[i] < kth) others = mass_add(others, Mass{key_value(list[i]), 1.0f}, c);
-      }
-    } else if constexpr (MODE != kLists) {
-      for (int j = tid; j < K; j += NT) s.sorted[j] = 0;
+      __syncthreads();
+      list = s.list;
     }
-    if constexpr (MODE == kLists) {
-      const int len = list_len(K);
-      for (int j = tid; j < len; j += NT) o.keys[(row * P + seg) * len + j] = j < nl ? list[j] : 0;
-    }
-
-    // ---- the segment's mass, outputs ----
+  }
+  if constexpr (MODE != kLists) {
+    write_best<NT, MODE>(list, nl, nl, K, others, bad, wmax, row, c, c64, bm, o, s.out);
+  } else {
+    const size_t part = row * P + seg;
+    const int len = list_len(K);
+    for (int j = tid; j < len; j += NT) o.keys[part * len + j] = j < nl ? list[j] : 0;
     others = wave_mass(others, c);
     if constexpr (NW > 1) {
       if (lane == 0) s.mass[wave] = others;
       __syncthreads();
-      if (wave == 0) others = wave_mass(lane < NW ? s.mass[lane] : mass_none(), c);
-    } else {
-      __syncthreads();
+      others = wave_mass(lane < NW ? s.mass[lane] : mass_none(), c);
     }
-    if constexpr (MODE == kRows) {
-      if (wave == 0) write_row(o, row, s.sorted, K, others, bad, c, c64);
-    } else if constexpr (MODE == kBeams) {
-      if (wave == 0) write_beam(bm, o, row, s.sorted, K, others, bad, c, c64);
-    } else {
-      if (tid == 0) o.parts[row * P + seg] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
-    }
-    __syncthreads();  // LDS is reused by the next item
+    if (tid == 0) o.parts[part] = bad ? Mass{neg_inf(), __builtin_nanf("")} : others;
   }
 }
 
@@ -510,195 +535,166 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
 // bound comes from the granules' maxima; candidates leave the registers, and one
 // pass of exponentials over what stays gives the others' mass.  Nothing is read
 // twice.
-constexpr int kSmallCand = 448;
+constexpr int kSmallCand = TopCaps<64>::kRank;
 
 template <typename T, int L, TopMode MODE>
-__global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ logits, int32_t R, int32_t V, int32_t K,
+__global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ logits, int32_t base, int32_t V, int32_t K,
                                                        float c, double c64, TopBeams bm, TopOut o) {
   constexpr int EPL = Row<T>::EPL;
   __shared__ uint64_t cand[kSmallCand + 4];
-  __shared__ uint64_t sorted[DSPARK_MAX_TOP];
+  __shared__ RankLds<64> out;
   const int lane = threadIdx.x;
   int step = 0;
-  for (int row = blockIdx.x; row < R; row += gridDim.x) {
-    const size_t at_row = static_cast<size_t>(row);
-    if (unread_beam<64, MODE>(bm, o, at_row, K)) continue;
-    const Row<T> r = make_row(logits + at_row * V, V);
-    uint4 u[L];
-    group_load<T, 64, L>(r, 0, lane, u);
-    float gm[L], lmax = neg_inf();
+  const size_t at_row = static_cast<size_t>(base) + blockIdx.x;
+  if (unread_beam<64, MODE>(bm, o, at_row, K)) return;
+  const Row<T> r = make_row(logits + at_row * V, V);
+  uint4 u[L];
+  group_load<T, 64, L>(r, 0, lane, u);
+  float gm[L], lmax = neg_inf();
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    gm[i] = neg_inf();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) gm[i] = fmaxf(gm[i], gran_elem(u[i], j, T{}));
+    lmax = fmaxf(lmax, gm[i]);
+  }
+  const float wmax = wave_max(lmax);
+  bool bad = wmax == pos_inf(), slow = false;
+  Mass others = mass_none();
+  int nl = 0;  // candidates listed
+  if (!bad && wmax > neg_inf()) {
+    // ---- bound: at least K granules (or all finite ones) reach it ----
+    const uint32_t kmax = order_key(wmax);
+    const float wmin = -wave_max(-lmax);
+    auto granules_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+      Count3 n{0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const uint32_t k = order_key(gm[i]);
+        n.a += __popcll(__ballot(k >= t1));
+        n.b += __popcll(__ballot(k >= t2));
+        n.c += __popcll(__ballot(k >= t3));
+      }
+      return n;
+    };
+    uint32_t bound = K <= 64 && wmin > neg_inf() ? order_key(wmin) : kKeyNegInf + 1;
+    int nb = granules_at(bound, bound, bound).a;
+    if (nb > K) bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), granules_at);
+    // ---- the elements that reach it leave the registers ----
+    const float at = key_value(bound);
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      gm[i] = neg_inf();
+      repack(u[i]);
+      if (__any(gm[i] >= at)) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) gm[i] = fmaxf(gm[i], gran_elem(u[i], j, T{}));
-      lmax = fmaxf(lmax, gm[i]);
+        for (int j = 0; j < EPL; ++j) mine += gran_elem(u[i], j, T{}) >= at;
+      }
     }
-    const float wmax = wave_max(lmax);
-    bool bad = wmax == pos_inf(), slow = false;
-    Mass others = mass_none();
-    int nl = 0;  // candidates listed
-    if (!bad && wmax > neg_inf()) {
-      // ---- bound: at least K granules (or all finite ones) reach it ----
-      const uint32_t kmax = order_key(wmax);
-      const float wmin = -wave_max(-lmax);
-      auto granules_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-        Count3 n{0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const uint32_t k = order_key(gm[i]);
-          n.a += __popcll(__ballot(k >= t1));
-          n.b += __popcll(__ballot(k >= t2));
-          n.c += __popcll(__ballot(k >= t3));
-        }
-        return n;
-      };
-      uint32_t bound = K <= 64 && wmin > neg_inf() ? order_key(wmin) : kKeyNegInf + 1;
-      int nb = granules_at(bound, bound, bound).a;
-      if (nb > K) bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), granules_at);
-      // ---- the elements that reach it leave the registers ----
-      const float at = key_value(bound);
-      int mine = 0;
+    int pos = block_scan<1>(mine, nullptr, nl);
+    slow = nl > kSmallCand;
+    if (slow) {
+      nl = exact_candidates<T, 64>(r, 0, r.Q, K, kmax, c, cand, nullptr, nullptr, step, others);
+    } else {
 #pragma unroll
       for (int i = 0; i < L; ++i) {
         repack(u[i]);
         if (__any(gm[i] >= at)) {
+          uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-          for (int j = 0; j < EPL; ++j) mine += gran_elem(u[i], j, T{}) >= at;
-        }
-      }
-      int pos = block_scan<1>(mine, nullptr, nl);
-      slow = nl > kSmallCand;
-      if (slow) {
-        nl = exact_candidates<T, 64>(r, 0, r.Q, K, kmax, c, cand, nullptr, nullptr, step, others);
-      } else {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          repack(u[i]);
-          if (__any(gm[i] >= at)) {
-            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-              const float x = gran_elem(u[i], j, T{});
-              if (x >= at) {
-                cand[pos++] = cand_key(order_key(x), (i * 64 + lane) * EPL - r.head + j);
-                if constexpr (sizeof(T) == 2)
-                  w[j / 2] = (j & 1) ? (w[j / 2] & 0x0000ffffu) | 0xFF800000u : (w[j / 2] & 0xffff0000u) | 0xFF80u;
-                else
-                  w[j] = 0xFF800000u;
-              }
+          for (int j = 0; j < EPL; ++j) {
+            const float x = gran_elem(u[i], j, T{});
+            if (x >= at) {
+              cand[pos++] = cand_key(order_key(x), (i * 64 + lane) * EPL - r.head + j);
+              if constexpr (sizeof(T) == 2)
+                w[j / 2] = (j & 1) ? (w[j / 2] & 0x0000ffffu) | 0xFF800000u : (w[j / 2] & 0xffff0000u) | 0xFF80u;
+              else
+                w[j] = 0xFF800000u;
             }
-            u[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          u[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __syncthreads();
       }
+      __syncthreads();
     }
-    if (!slow) {
-#pragma unroll
-      for (int i = 0; i < L; i += 4) {
-        uint4 v[4] = {u[i], u[i + 1], u[i + 2], u[i + 3]};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) repack(v[k]);
-        others = mass_add(others, group_mass<T, 4>(v, c), c);
-      }
-    }
-    rank_keys<64>(cand, nl, K, sorted);
-    const uint64_t kth = sorted[K - 1];
-    for (int i = lane; i < nl; i += 64)
-      if (cand[i] < kth) others = mass_add(others, Mass{key_value(cand[i]), 1.0f}, c);
-    others = wave_mass(others, c);
-    bad |= !(others.s >= 0.0f);
-    if constexpr (MODE == kRows)
-      write_row(o, at_row, sorted, K, others, bad, c, c64);
-    else
-      write_beam(bm, o, at_row, sorted, K, others, bad, c, c64);
-    __syncthreads();  // LDS is reused by the next row
   }
+  if (!slow) {
+#pragma unroll
+    for (int i = 0; i < L; i += 4) {
+      uint4 v[4] = {u[i], u[i + 1], u[i + 2], u[i + 3]};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) repack(v[k]);
+      others = mass_add(others, group_mass<T, 4>(v, c), c);
+    }
+  }
+  write_best<64, MODE>(cand, nl, nl, K, others, bad, wmax, at_row, c, c64, bm, o, out);
 }
 
 // The K best of the candidates of a row's P segments (in: their lists), one
 // workgroup a row; kRows or kBeams.
 template <TopMode MODE>
 __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t* __restrict__ in,
-                                                                  const Mass* __restrict__ parts, int32_t R, int32_t K,
+                                                                  const Mass* __restrict__ parts, int32_t base, int32_t K,
                                                                   int32_t P, float c, double c64, TopBeams bm,
                                                                   TopOut o) {
   constexpr int NT = kMergeThreads, NW = NT / 64;
   extern __shared__ uint64_t all[];  // P list_len(K) keys and 4 more
   __shared__ uint64_t list[kMaxList + 4];
-  __shared__ uint64_t sorted[DSPARK_MAX_TOP];
-  __shared__ int slots[6 * NW];
+  __shared__ RankLds<NT> out;
+  __shared__ uint64_t slots[2 * NW];
   __shared__ int scan[2][NW];
   __shared__ uint64_t red[2][NW];
-  __shared__ Mass shm[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int len = list_len(K), n = P * len;
   int step = 0;
-  for (int row = blockIdx.x; row < R; row += gridDim.x) {
-    const size_t at = static_cast<size_t>(row);
-    if (unread_beam<NT, MODE>(bm, o, at, K)) continue;
-    uint64_t top = 0, low = ~0ull;
-    int found = 0;
-    for (int i = tid; i < n; i += NT) {
-      const uint64_t k = in[at * n + i];
-      all[i] = k;
-      top = max(top, k);
-      if (k) low = min(low, k);
-      found += k != 0;
-    }
-    Mass others = mass_none();
-    for (int p = tid; p < P; p += NT) others = mass_add(others, parts[at * P + p], c);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
-      low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
-    }
-    if (lane == 0) {
-      red[0][wave] = top;
-      red[1][wave] = low;
-    }
-    block_scan<NW>(found, scan[0], found);  // its barrier completes all and red
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      top = max(top, red[0][w]);
-      low = min(low, red[1][w]);
-    }
-    uint64_t* best = all;
-    int nl = n;
-    if (n > 2 * list_len(K)) {
-      const uint64_t t = list_bound<NT>(all, n, found, K, found ? low : 1, top + 1, slots, step);
-      int mine = 0;
-      for (int i = tid; i < n; i += NT) mine += all[i] >= t;
-      int pos = block_scan<NW>(mine, scan[1], nl);
-      for (int i = tid; i < n; i += NT) {
-        const uint64_t k = all[i];
-        if (k >= t) {
-          list[pos++] = k;
-        } else if (k) {
-          others = mass_add(others, Mass{key_value(k), 1.0f}, c);
-        }
-      }
-      __syncthreads();
-      best = list;
-    }
-    rank_keys<NT>(best, nl, K, sorted);
-    const uint64_t kth = sorted[K - 1];
-    for (int i = tid; i < nl; i += NT)
-      if (best[i] != 0 && best[i] < kth) others = mass_add(others, Mass{key_value(best[i]), 1.0f}, c);
-    others = wave_mass(others, c);
-    if (lane == 0) shm[wave] = others;
-    __syncthreads();
-    if (wave == 0) {
-      others = wave_mass(lane < NW ? shm[lane] : mass_none(), c);
-      const bool bad = !(others.s >= 0.0f);
-      if constexpr (MODE == kRows)
-        write_row(o, at, sorted, K, others, bad, c, c64);
-      else
-        write_beam(bm, o, at, sorted, K, others, bad, c, c64);
-    }
-    __syncthreads();
+  const size_t at = static_cast<size_t>(base) + blockIdx.x;
+  if (unread_beam<NT, MODE>(bm, o, at, K)) return;
+  uint64_t top = 0, low = ~0ull;
+  int found = 0;
+  for (int i = tid; i < n; i += NT) {
+    const uint64_t k = in[at * n + i];
+    all[i] = k;
+    top = max(top, k);
+    if (k) low = min(low, k);
+    found += k != 0;
   }
+  Mass others = mass_none();
+  for (int p = tid; p < P; p += NT) others = mass_add(others, parts[at * P + p], c);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
+    low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
+  }
+  if (lane == 0) {
+    red[0][wave] = top;
+    red[1][wave] = low;
+  }
+  block_scan<NW>(found, scan[0], found);  // its barrier completes all and red
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    top = max(top, red[0][w]);
+    low = min(low, red[1][w]);
+  }
+  uint64_t* best = all;
+  int nl = n;
+  if (n > 2 * list_len(K)) {
+    const uint64_t t = list_bound<NT>(all, n, found, K, found ? low : 1, top + 1, slots, step);
+    int mine = 0;
+    for (int i = tid; i < n; i += NT) mine += all[i] >= t;
+    int pos = block_scan<NW>(mine, scan[1], nl);
+    for (int i = tid; i < n; i += NT) {
+      const uint64_t k = all[i];
+      if (k >= t) {
+        list[pos++] = k;
+      } else if (k) {
+        others = mass_add(others, Mass{key_value(k), 1.0f}, c);
+      }
+    }
+    __syncthreads();
+    best = list;
+  }
+  const int nv = best == all ? found : nl;
+  write_best<NT, MODE>(best, nl, nv, K, others, false, found ? key_value(top) : neg_inf(), at, c, c64, bm, o, out);
 }
 
 // Rows are cut into segments of `groups` groups a thread; groups = 0: short rows,
@@ -706,14 +702,13 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
 TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
   // granules of a row, at the least favourable alignment
   const int q = any ? (V + 2 * epl - 2) / epl : V / epl;
-  const int kL = 32 / epl;
   TopSplit s{};
   s.P = 1;
   if (q <= 8 * 64) {
     s.NT = q <= 4 * 64 ? 4 : 8;
     return s;
   }
-  int most;
+  int most, kL = 4;
   if (q <= TopCaps<64>::kG * 64 * kL && R >= 2048 && K <= 32) {
     s.NT = 64;
     most = TopCaps<64>::kG;
@@ -724,6 +719,10 @@ TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
     s.NT = 256;
     most = TopCaps<256>::kG;
   }
+  // float32 rows too long for one segment of 4 granules a group take 8: the
+  // groups then hold 32 logits, as those of bf16 do
+  if (epl == 4 && q > most * s.NT * kL) kL = 8;
+  s.L = kL;
   const int need = (q + s.NT * kL - 1) / (s.NT * kL);  // groups of a thread over the row
   s.P = (need + most - 1) / most;
   s.groups = (need + s.P - 1) / s.P;
@@ -734,16 +733,24 @@ template <typename T, TopMode MODE>
 hipError_t launch_segments(const T* logits, int32_t R, int32_t V, int32_t K, const TopSplit& sp, float c, double c64,
                            const TopBeams& bm, const TopOut& o, hipStream_t st) {
   const int64_t items = static_cast<int64_t>(R) * sp.P;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid)));
-#define DSPARK_TOP(NT)                                                                                              \
-  DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, NT, MODE>), grid, dim3(NT), 0, st, logits, items, V, K, sp.P, \
+#define DSPARK_TOP(NT, L)                                                                                               \
+  DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, NT, L, MODE>), grid, dim3(NT), 0, st, logits, base, V, K, sp.P, \
                 sp.groups, c, c64, bm, o)
-  if (sp.NT == 64)
-    DSPARK_TOP(64);
-  else if (sp.NT == 256)
-    DSPARK_TOP(256);
-  else
-    DSPARK_TOP(512);
+  for (int64_t base = 0; base < items; base += kMaxGrid) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));
+    if (sp.NT == 64)
+      DSPARK_TOP(64, 4);
+    else if (sp.L == 4 && sp.NT == 256)
+      DSPARK_TOP(256, 4);
+    else if (sp.L == 4)
+      DSPARK_TOP(512, 4);
+    else if constexpr (sizeof(T) == 4) {
+      if (sp.NT == 256)
+        DSPARK_TOP(256, 8);
+      else
+        DSPARK_TOP(512, 8);
+    }
+  }
 #undef DSPARK_TOP
   return hipGetLastError();
 }
@@ -751,13 +758,16 @@ hipError_t launch_segments(const T* logits, int32_t R, int32_t V, int32_t K, con
 template <typename T, TopMode MODE>
 hipError_t launch_small(const T* logits, int32_t R, int32_t V, int32_t K, const TopSplit& sp, float c, double c64,
                         const TopBeams& bm, const TopOut& o, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(std::min(R, kMaxGrid)));
 #define DSPARK_SMALL(L)                                                                                             \
-  DSPARK_LAUNCH("top_small", (top_small_kernel<T, L, MODE>), grid, dim3(64), 0, st, logits, R, V, K, c, c64, bm, o)
-  if (sp.NT == 4)
-    DSPARK_SMALL(4);
-  else
-    DSPARK_SMALL(8);
+  DSPARK_LAUNCH("top_small", (top_small_kernel<T, L, MODE>), grid, dim3(64), 0, st, logits, base, V, K, c, c64, bm, o)
+  for (int32_t base = 0, n; base < R; base += n) {
+    n = std::min(R - base, kMaxGrid);
+    const dim3 grid(static_cast<unsigned>(n));
+    if (sp.NT == 4)
+      DSPARK_SMALL(4);
+    else
+      DSPARK_SMALL(8);
+  }
 #undef DSPARK_SMALL
   return hipGetLastError();
 }
@@ -782,9 +792,12 @@ hipError_t launch_rows(const void* logits, int dtype, int32_t R, int32_t V, int3
   const hipError_t e = dtype == DSPARK_BF16 ? launch_segments<uint16_t, kLists>(h, R, V, K, sp, c, c64, bm, part, st)
                                             : launch_segments<float, kLists>(f, R, V, K, sp, c, c64, bm, part, st);
   if (e != hipSuccess) return e;
-  DSPARK_LAUNCH("top_merge", (top_merge_kernel<MODE>), dim3(static_cast<unsigned>(std::min(R, kMaxGrid))),
-                dim3(kMergeThreads), (static_cast<size_t>(sp.P) * list_len(K) + 4) * sizeof(uint64_t), st, lists, parts,
-                R, K, sp.P, c, c64, bm, o);
+  for (int32_t base = 0, n; base < R; base += n) {
+    n = std::min(R - base, kMaxGrid);
+    DSPARK_LAUNCH("top_merge", (top_merge_kernel<MODE>), dim3(static_cast<unsigned>(n)), dim3(kMergeThreads),
+                  (static_cast<size_t>(sp.P) * list_len(K) + 4) * sizeof(uint64_t), st, lists, parts, base, K, sp.P, c,
+                  c64, bm, o);
+  }
   return hipGetLastError();
 }
 
