@@ -29,7 +29,7 @@ constexpr int kFinalThreads = 256;
 constexpr int kFinalWaves = kFinalThreads / 64;
 constexpr int kMaxCand = DSPARK_MAX_BEAMS * DSPARK_MAX_TOP;
 constexpr int kRankAll = 128;   // candidates ranked at once; more are first cut by a search
-constexpr int kMaxGrid = 1 << 20;
+constexpr int kMaxGrid = 1 << 22;  // workgroups of a launch; more are further launches
 
 __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ sums,
                                                                    const uint64_t* __restrict__ keys, int32_t base,
@@ -133,71 +133,96 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
 }
 
 // ---- reordering -------------------------------------------------------------------
-// Unit: the widest of 16, 4, 2 and 1 bytes that divides every extent and
-// address.  A row of a beam is S runs of T tokens of U units; only the tokens
-// before the request's length move.  One workgroup moves a stretch of units of
-// one run of every beam of a request: MB children at a time, all of them
-// loaded before any is stored (in place: MB >= M).
+// A row of a beam is S runs of T tokens; only the tokens before the request's
+// length move.  Runs that are multiples of 16 bytes at 16-byte addresses move in
+// 16-byte units, the last bytes of a length singly; others in the widest of 4, 2
+// and 1 bytes that divides token and address.  One workgroup moves a stretch of
+// units of one run of every beam of a request: MB children at a time, all of them
+// loaded before any is stored (in place: MB >= M).  16-byte stores are
+// non-temporal (1.6 GB of caches: 508 us, 5.7 TB/s, against 563; non-temporal
+// loads slow it down: a parent's children then read it again).
 constexpr int kMoveThreads = 256;
 
+template <typename U>
+__device__ __forceinline__ void put(U* p, U v) {
+  if constexpr (sizeof(U) == 16)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 template <typename U, int MB>
-__global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const U* src, U* dst,
+__global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const char* src, char* dst,
                                                                     const int32_t* __restrict__ parents,
-                                                                    const int32_t* __restrict__ lengths, int64_t items,
+                                                                    const int32_t* __restrict__ lengths, int64_t base,
                                                                     int64_t chunks, int32_t B, int32_t W, int32_t M,
-                                                                    int32_t S, int32_t T, int64_t unit, bool in_place) {
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t run = item / chunks;
-    const int64_t chunk = item - run * chunks;
-    const int s = static_cast<int>(run % S);
-    const int64_t lb = run / S;
-    const int b = static_cast<int>(lb % B);
-    int64_t t = T;
-    if (lengths) t = min(max(lengths[b], 0), T);
-    const int64_t used = t * unit;
-    const int64_t at = chunk * kMoveThreads + threadIdx.x;
-    const int64_t seg = static_cast<int64_t>(T) * unit, row = seg * S;
-    if (at >= used) continue;
-    const U* from = src + lb * W * row + s * seg + at;
-    U* to = dst + lb * M * row + s * seg + at;
-    for (int j0 = 0; j0 < M; j0 += MB) {
-      U v[MB];
-      int p[MB];
+                                                                    int32_t S, int32_t T, int64_t token,
+                                                                    bool in_place) {
+  constexpr int64_t kU = sizeof(U);
+  const int64_t item = base + blockIdx.x;
+  const int64_t run = item / chunks, chunk = item - run * chunks;
+  const int64_t lb = run / S;
+  const int s = static_cast<int>(run - lb * S);
+  const int b = static_cast<int>(lb % B);
+  int64_t t = T;
+  if (lengths) t = min(max(lengths[b], 0), T);
+  const int64_t at = (chunk * kMoveThreads + threadIdx.x) * kU, left = t * token - at;
+  if (left <= 0) return;
+  const int64_t seg = static_cast<int64_t>(T) * token, row = seg * S;
+  const char* from = src + lb * W * row + s * seg + at;
+  char* to = dst + lb * M * row + s * seg + at;
+  for (int j0 = 0; j0 < M; j0 += MB) {
+    int p[MB];
 #pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        p[j] = -1;
-        if (j0 + j < M) p[j] = parents[static_cast<int64_t>(b) * M + j0 + j];
-        if (p[j] >= W || (in_place && p[j] == j0 + j)) p[j] = -1;
-        if (p[j] >= 0) v[j] = from[p[j] * row];
-      }
+    for (int j = 0; j < MB; ++j) {
+      p[j] = -1;
+      if (j0 + j < M) p[j] = parents[static_cast<int64_t>(b) * M + j0 + j];
+      if (p[j] >= W || (in_place && p[j] == j0 + j)) p[j] = -1;
+    }
+    if (left >= kU) {
+      U v[MB];
 #pragma unroll
       for (int j = 0; j < MB; ++j)
-        if (p[j] >= 0) to[(j0 + j) * row] = v[j];
+        if (p[j] >= 0) v[j] = *reinterpret_cast<const U*>(from + p[j] * row);
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+        if (p[j] >= 0) put(reinterpret_cast<U*>(to + (j0 + j) * row), v[j]);
+    } else {
+      for (int64_t i = 0; i < left; ++i) {
+        char v[MB];
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          if (p[j] >= 0) v[j] = from[p[j] * row + i];
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          if (p[j] >= 0) to[(j0 + j) * row + i] = v[j];
+      }
     }
   }
 }
 
 template <typename U>
 hipError_t move(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L, int32_t B,
-                int32_t W, int32_t M, int32_t S, int32_t T, int64_t bytes, hipStream_t st) {
-  const int64_t unit = bytes / static_cast<int64_t>(sizeof(U));
-  const int64_t chunks = (T * unit + kMoveThreads - 1) / kMoveThreads;
+                int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st) {
+  const int64_t chunks = (T * token / static_cast<int64_t>(sizeof(U)) + kMoveThreads - 1) / kMoveThreads;
   const int64_t items = L * B * S * chunks;
   const bool in_place = src == dst;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, kMaxGrid)));
-  const U* s = static_cast<const U*>(src);
-  U* d = static_cast<U*>(dst);
-#define DSPARK_MOVE(MB)                                                                                            \
+  const char* s = static_cast<const char*>(src);
+  char* d = static_cast<char*>(dst);
+#define DSPARK_MOVE(MB)                                                                                        \
   DSPARK_LAUNCH("beam_reorder", (beam_reorder_kernel<U, MB>), grid, dim3(kMoveThreads), 0, st, s, d, parents, \
-                lengths, items, chunks, B, W, M, S, T, unit, in_place)
-  if (M <= 4)
-    DSPARK_MOVE(4);
-  else if (M <= 8 || !in_place)
-    DSPARK_MOVE(8);
-  else if (M <= 16)
-    DSPARK_MOVE(16);
-  else
-    DSPARK_MOVE(32);
+                lengths, base, chunks, B, W, M, S, T, token, in_place)
+  for (int64_t base = 0; base < items; base += kMaxGrid) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));
+    if (M <= 4)
+      DSPARK_MOVE(4);
+    else if (M <= 8 || !in_place)
+      DSPARK_MOVE(8);
+    else if (M <= 16)
+      DSPARK_MOVE(16);
+    else
+      DSPARK_MOVE(32);
+  }
 #undef DSPARK_MOVE
   return hipGetLastError();
 }
@@ -237,12 +262,13 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
 }
 
 hipError_t launch_beam_reorder(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L,
-                               int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t bytes, hipStream_t st) {
-  const uintptr_t all = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | static_cast<uintptr_t>(bytes);
-  if (all % 16 == 0) return move<u32x4>(src, dst, parents, lengths, L, B, W, M, S, T, bytes, st);
-  if (all % 4 == 0) return move<uint32_t>(src, dst, parents, lengths, L, B, W, M, S, T, bytes, st);
-  if (all % 2 == 0) return move<uint16_t>(src, dst, parents, lengths, L, B, W, M, S, T, bytes, st);
-  return move<uint8_t>(src, dst, parents, lengths, L, B, W, M, S, T, bytes, st);
+                               int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst);
+  const uintptr_t all = at | static_cast<uintptr_t>(token);
+  if (at % 16 == 0 && T * token % 16 == 0) return move<u32x4>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
+  if (all % 4 == 0) return move<uint32_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
+  if (all % 2 == 0) return move<uint16_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
+  return move<uint8_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
 }
 
 }  // namespace dspark

@@ -199,7 +199,7 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
                               int32_t B, int32_t W, int32_t V, int32_t M, int32_t* tokens, int32_t* parents,
                               float* out_scores, uint8_t* flags, void* ws, const BeamPlan& pl, hipStream_t st);
 hipError_t launch_beam_reorder(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L,
-                               int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t bytes, hipStream_t st);
+                               int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st);
 
 hipError_t launch_markov(const void* backbone, int dtype, const int32_t* anchor,
                          const uint16_t* w1, const uint16_t* w2, const uint16_t* hidden,

@@ -79,14 +79,18 @@ __device__ __forceinline__ uint4 gran_load(const Row<T>& r, int q) {
 __device__ __forceinline__ void repack(uint4& u) { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }
 
 // L granules per thread, q0 + i NT + tid: one branch on the whole group (uniform)
-// keeps the interior loads free of per-lane checks.
-template <typename T, int NT, int L>
+// keeps the interior loads free of per-lane checks.  ONCE: non-temporal loads.
+template <typename T, int NT, int L, bool ONCE = false>
 __device__ __forceinline__ void group_load(const Row<T>& r, int q0, int tid, uint4 (&u)[L]) {
   constexpr int EPL = Row<T>::EPL;
   if ((q0 > 0 || r.head == 0) && (q0 + NT * L) * EPL - r.head <= r.V) {
     const T* p = r.p + (static_cast<ptrdiff_t>(q0 + tid) * EPL - r.head);
 #pragma unroll
-    for (int i = 0; i < L; ++i) u[i] = *reinterpret_cast<const uint4*>(p + i * NT * EPL);
+    for (int i = 0; i < L; ++i) {
+      const u32x4* a = reinterpret_cast<const u32x4*>(p + i * NT * EPL);
+      const u32x4 v = ONCE ? __builtin_nontemporal_load(a) : *a;
+      u[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
   } else {
     // the whole granules first, all in flight together; others read the row's
     // first whole granule in their place
