@@ -130,16 +130,43 @@ struct Mass {
 __device__ __forceinline__ Mass mass_none() { return Mass{neg_inf(), 0.0f}; }
 
 // Exponent by which a mass relative to m becomes one relative to n >= m.
-// The products are rounded by themselves, as in the sums.
+// The products are rounded by themselves, as in the sums (where m c overflows
+// and n c does not, it is -inf, as it should be).
 __device__ __forceinline__ float mass_gap(float m, float n, float c) {
 #pragma clang fp contract(off)
-  return fabsf(n) > kHugeLogit || fabsf(m) > kHugeLogit ? (m - n) * c : m * c - n * c;
+  return fabsf(n) > kHugeLogit ? (m - n) * c : m * c - n * c;
 }
 
 __device__ __forceinline__ Mass mass_add(Mass a, Mass b, float c) {
+#pragma clang fp contract(off)
   const float n = fmaxf(a.m, b.m);
   if (n == neg_inf()) return Mass{n, a.s + b.s};  // 0, or the NaN of either
-  return Mass{n, a.s * __builtin_amdgcn_exp2f(mass_gap(a.m, n, c)) + b.s * __builtin_amdgcn_exp2f(mass_gap(b.m, n, c))};
+  float ga = a.m * c - n * c, gb = b.m * c - n * c;
+  if (fabsf(n) > kHugeLogit) {
+    ga = (a.m - n) * c;
+    gb = (b.m - n) * c;
+  }
+  return Mass{n, a.s * __builtin_amdgcn_exp2f(ga) + b.s * __builtin_amdgcn_exp2f(gb)};
+}
+
+// The N masses m[i] for which take[i], as one (s = 0 where there is none).
+template <int N>
+__device__ __forceinline__ Mass mass_sum(const Mass (&m)[N], uint32_t take, float c) {
+#pragma clang fp contract(off)
+  float n = neg_inf(), s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) n = fmaxf(n, (take >> i) & 1u ? m[i].m : neg_inf());
+  if (__any(fabsf(n) > kHugeLogit && n > neg_inf())) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      s += ((take >> i) & 1u) && m[i].m > neg_inf() ? m[i].s * __builtin_amdgcn_exp2f(mass_gap(m[i].m, n, c)) : 0.0f;
+  } else {
+    const float r = n > neg_inf() ? n * c : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      s += (take >> i) & 1u ? m[i].s * __builtin_amdgcn_exp2f(m[i].m * c - r) : 0.0f;
+  }
+  return Mass{n, s};
 }
 
 // Mass of L granules held by one thread.

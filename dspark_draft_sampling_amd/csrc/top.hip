@@ -119,14 +119,16 @@ __device__ __forceinline__ uint64_t list_bound(const uint64_t* cand, int n, int 
 template <int NT>
 struct RankLds {
   uint16_t rank[TopCaps<NT>::kRank];
-  Mass others[NT / 64], top[NT / 64];
+  Mass others[NT / 64];
+  float top[NT / 64];
   double sum[NT / 64];
 };
 
 // Outputs of a row or beam from its n candidates in LDS (distinct keys, 0s
-// among them are none, room for 4 more; nv of them are not 0) and the threads'
+// among them are none; nv of them are not 0) and the threads'
 // shares of the mass of all other elements.  A candidate's rank is the number of
 // greater keys; those below K are the outputs, the others' mass joins the rest.
+// list is complete, with 4 zeros after it.
 // wmax: the row's largest value.  bad, or a NaN mass: a NaN or +inf was seen.
 // A beam's normaliser is formed in 64 bits, its K best tokens one by one.
 template <int NT, TopMode MODE>
@@ -135,9 +137,7 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
                                            RankLds<NT>& s) {
   constexpr int NW = NT / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  if (tid < 4) list[n + tid] = 0;
-  __syncthreads();
-  Mass top = mass_none();
+  float top = 0.0f;  // mass of the outputs relative to wmax
   double sum = 0.0;
   for (int i = tid; i < n; i += NT) {
     const uint64_t k = list[i];
@@ -155,14 +155,14 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
     } else if constexpr (MODE == kRows) {
       o.values[row * K + rank] = x;
       o.ids[row * K + rank] = key_index(k);
-      top = mass_add(top, Mass{x, 1.0f}, c);
+      top += __builtin_amdgcn_exp2f(mass_gap(x, wmax, c));
     } else {
       sum += exp2((static_cast<double>(x) - static_cast<double>(wmax)) * c64);
     }
   }
   others = wave_mass(others, c);
   if constexpr (MODE == kRows)
-    top = wave_mass(top, c);
+    top = wave_sum(top);
   else
     sum = wave_sum64(sum);
   if constexpr (NW > 1) {
@@ -176,7 +176,9 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
     __syncthreads();
     others = wave_mass(lane < NW ? s.others[lane] : mass_none(), c);
     if constexpr (MODE == kRows) {
-      top = wave_mass(lane < NW ? s.top[lane] : mass_none(), c);
+      top = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top += s.top[w];
     } else {
       sum = 0.0;
 #pragma unroll
@@ -193,7 +195,7 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
     }
     if (tid == 0) {
       const double r = mass_log2(others, c, c64);
-      const double l = log2_add(r, mass_log2(top, c, c64));
+      const double l = log2_add(r, mass_log2(Mass{wmax, top}, c, c64));
       const float nan = __builtin_nanf("");
       o.rest[row] = bad ? nan : static_cast<float>(r * 0.69314718055994530942);
       o.lse[row] = bad ? nan : static_cast<float>(l * 0.69314718055994530942);
@@ -230,10 +232,17 @@ __device__ __forceinline__ Mass gran_mass(const uint4& u, int e0, float c, F&& k
     if (!keep(x[j], e0 + j)) x[j] = neg_inf();
     m = fmaxf(m, x[j]);
   }
-  const float ref = m > neg_inf() ? m : 0.0f;
   float s = 0.0f;  // a NaN, too, ends up here
+  if (__any(fabsf(m) > kHugeLogit && m > neg_inf())) {
+    const float ref = m > neg_inf() ? m : 0.0f;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) s += __builtin_amdgcn_exp2f(mass_gap(x[j], ref, c));
+    for (int j = 0; j < EPL; ++j)
+      s += __builtin_amdgcn_exp2f(fabsf(ref) > kHugeLogit ? (x[j] - ref) * c : fmaf(x[j], c, -(ref * c)));
+  } else {
+    const float r = m > neg_inf() ? m * c : 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s += __builtin_amdgcn_exp2f(fmaf(x[j], c, -r));
+  }
   return Mass{m, s};
 }
 
@@ -328,6 +337,7 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
       if (k >= kth && x > neg_inf()) cand[pos++] = k;
     }
   }
+  if (tid < 4) cand[total + tid] = 0;
   __syncthreads();
   return total;
 }
@@ -429,33 +439,32 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
     const float at = key_value(bound);
 
     // ---- the groups at the bound, in thread order; the mass of the others ----
-    Mass m[G];  // all of them at once, so that the reads overlap
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      m[g] = s.grp[min(g, n - 1) * NT + tid];
-      if (g >= n) m[g] = mass_none();
-    }
+    uint32_t in = 0;  // bit g: group g is at the bound
     int mine = 0;
-    float om = neg_inf(), os = 0.0f;
+    Mass share[G / 4];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      mine += m[g].m >= at;
-      om = fmaxf(om, m[g].m >= at ? neg_inf() : m[g].m);
+    for (int g0 = 0; g0 < G; g0 += 4) {
+      share[g0 / 4] = mass_none();
+      if (g0 < n) {
+        Mass m[4];  // the reads overlap
+        uint32_t out = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[k] = s.grp[min(g0 + k, n - 1) * NT + tid];
+          const bool ok = g0 + k < n, at_bound = ok && m[k].m >= at;
+          in |= at_bound ? 1u << (g0 + k) : 0u;
+          out |= ok && !at_bound ? 1u << k : 0u;
+        }
+        share[g0 / 4] = mass_sum<4>(m, out, c);
+      }
     }
+    mine = __popc(in);
     int nq;
     int pos = block_scan<NW>(mine, s.scan[0], nq);
     const bool fits = nq <= QUAL;
-    if (mine > 0 && fits) {
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        if (m[g].m >= at) s.qual[pos++] = static_cast<uint16_t>(g * NT + tid);
-    }
-    if (om > neg_inf()) {
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        os += (m[g].m >= at ? 0.0f : m[g].s) * __builtin_amdgcn_exp2f(fminf(mass_gap(m[g].m, om, c), 0.0f));
-    }
-    others = Mass{om, os};
+    if (fits)
+      for (; in != 0; in &= in - 1) s.qual[pos++] = static_cast<uint16_t>((__ffs(in) - 1) * NT + tid);
+    others = mass_sum<G / 4>(share, (1u << (G / 4)) - 1, c);
     __syncthreads();
 
     // ---- candidates: their elements at or above the bound, in thread order ----
@@ -491,6 +500,7 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
           }
         }
       }
+      if (nc <= CAND && tid < 4) s.cand[nc + tid] = 0;
       __syncthreads();
     }
     if (nc > CAND) nc = exact_candidates<T, NT>(r, first, q1, K, kmax, c, s.cand, s.slots, s.scan[0], step, others);
@@ -511,6 +521,7 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
           others = mass_add(others, Mass{key_value(k), 1.0f}, c);
         }
       }
+      if (tid < 4) s.list[nl + tid] = 0;
       __syncthreads();
       list = s.list;
     }
@@ -615,6 +626,7 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
           u[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      if (lane < 4) cand[nl + lane] = 0;
       __syncthreads();
     }
   }
@@ -665,6 +677,7 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
     top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), d, 64)));
     low = min(low, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(low), d, 64)));
   }
+  if (tid < 4) all[n + tid] = 0;
   if (lane == 0) {
     red[0][wave] = top;
     red[1][wave] = low;
@@ -690,6 +703,7 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
         others = mass_add(others, Mass{key_value(k), 1.0f}, c);
       }
     }
+    if (tid < 4) list[nl + tid] = 0;
     __syncthreads();
     best = list;
   }
