@@ -118,17 +118,19 @@ __device__ __forceinline__ Entries<ENT> load_entries(const Row<T>& r, const Dist
   return e;
 }
 
-// Everything in base-2 logarithms and 64 bits.
+// In 64 bits, logarithms to base 2.  The teacher's weights are et / st, relative to
+// 2^rt, the draft's es / ss, relative to 2^rs.
 template <int ENT>
 struct Outcomes {
-  double lt[ENT];   // log2 t_j (-inf: no such entry)
-  double ls[ENT];   // log2 s at its token
-  double lt_r, ls_r;  // everything else
-  double lse;       // log2 of the draft's whole mass
-  uint32_t first;   // bit i: no earlier entry of the row has entry i's token
-  bool twice;       // some token is listed more than once
-  bool bad;         // a NaN or +inf
-  bool empty;       // no mass on one side
+  double zt[ENT], zs[ENT];  // logits (-inf: no such entry)
+  double et[ENT], es[ENT];
+  double zr;                // the teacher's logit of everything else
+  double et_r, es_r;
+  double rt, rs, st, ss;
+  uint32_t first;  // bit i: no earlier entry of the row has entry i's token
+  bool twice;      // some token is listed more than once
+  bool bad;        // a NaN or +inf
+  bool empty;      // no mass on one side
 };
 
 template <int ENT>
@@ -139,7 +141,7 @@ __device__ __forceinline__ Outcomes<ENT> outcomes(const Entries<ENT>& e, int K, 
   Outcomes<ENT> o;
   bool bad = isnan(rest2) || rest2 == __builtin_inf() || !(e.trest < pos_inf());
   // the largest values, as references (in 32 bits: they only set the scale)
-  const double zr = static_cast<double>(e.trest) * kLog2ed;
+  o.zr = static_cast<double>(e.trest) * kLog2ed;
   float mt = neg_inf(), ms = neg_inf();
 #pragma unroll
   for (int i = 0; i < ENT; ++i) {
@@ -173,30 +175,29 @@ __device__ __forceinline__ Outcomes<ENT> outcomes(const Entries<ENT>& e, int K, 
       for (int i = 0; i < ENT; ++i)
         if (id == e.id[i] && j < i * 64 + lane) o.first &= ~(1u << i);
     }
-  const double nt = fmax(static_cast<double>(wave_max(mt)) * c64, zr);
+  const double nt = fmax(static_cast<double>(wave_max(mt)) * c64, o.zr);
   const double ns = fmax(static_cast<double>(wave_max(ms)) * c64, rest2);
-  const double rt = nt == -__builtin_inf() ? 0.0 : nt, rs = ns == -__builtin_inf() ? 0.0 : ns;
-  double st = 0.0, ss = 0.0, zt[ENT], zs[ENT];
+  o.rt = nt == -__builtin_inf() ? 0.0 : nt;
+  o.rs = ns == -__builtin_inf() ? 0.0 : ns;
+  double st = 0.0, ss = 0.0;
 #pragma unroll
   for (int i = 0; i < ENT; ++i) {
-    zt[i] = static_cast<double>(e.v[i]) * c64;
-    zs[i] = static_cast<double>(e.x[i]) * c64;
-    st += exp2(zt[i] - rt);
-    if ((o.first >> i) & 1u) ss += exp2(zs[i] - rs);
+    o.zt[i] = static_cast<double>(e.v[i]) * c64;
+    o.zs[i] = static_cast<double>(e.x[i]) * c64;
+    o.et[i] = e.v[i] > neg_inf() ? exp2_64(o.zt[i] - o.rt) : 0.0;
+    o.es[i] = e.x[i] > neg_inf() ? exp2_64(o.zs[i] - o.rs) : 0.0;
+    st += o.et[i];
+    if ((o.first >> i) & 1u) ss += o.es[i];
   }
-  st = wave_sum64(st) + exp2(zr - rt);
-  ss = wave_sum64(ss) + exp2(rest2 - rs);
+  // everything else: the teacher's side on lane 0, the draft's on lane 1
+  const double zl = lane == 0 ? o.zr : rest2;
+  const double el = zl > -__builtin_inf() ? exp2_64(zl - (lane == 0 ? o.rt : o.rs)) : 0.0;
+  o.et_r = lane_d(el, 0);
+  o.es_r = lane_d(el, 1);
+  o.st = wave_sum64(st) + o.et_r;
+  o.ss = wave_sum64(ss) + o.es_r;
   o.bad = __any(bad);
-  o.empty = !(st > 0.0) || !(ss > 0.0);
-  const double lt = rt + log2(st);
-  o.lse = rs + log2(ss);
-#pragma unroll
-  for (int i = 0; i < ENT; ++i) {
-    o.lt[i] = zt[i] - lt;
-    o.ls[i] = zs[i] - o.lse;
-  }
-  o.lt_r = zr - lt;
-  o.ls_r = rest2 - o.lse;
+  o.empty = !(o.st > 0.0) || !(o.ss > 0.0);
   return o;
 }
 
@@ -263,20 +264,21 @@ template <int ENT>
 __device__ __forceinline__ float finish_row(const Entries<ENT>& e, const DistillArgs& a, size_t row, double rest2,
                                             int32_t* sh_ids, const LossOut& out) {
   const Outcomes<ENT> o = outcomes<ENT>(e, a.K, rest2, a.c64, sh_ids);
+  // sum t (log t - log s) with log t = z - rt - log st, log s = z - rs - log ss
   double k = 0.0;
 #pragma unroll
-  for (int i = 0; i < ENT; ++i) {
-    const double t = exp2(o.lt[i]);
-    if (t > 0.0) k += t * (o.lt[i] - o.ls[i]);
-  }
+  for (int i = 0; i < ENT; ++i)
+    if (o.et[i] > 0.0) k += o.et[i] * (o.zt[i] - o.zs[i]);
   k = wave_sum64(k);
-  const double tr = exp2(o.lt_r);
-  if (tr > 0.0) k += tr * (o.lt_r - o.ls_r);
+  if (o.et_r > 0.0) k += o.et_r * (o.zr - rest2);
+  k = k / o.st - (o.rt - o.rs) + log2_64(o.ss / o.st);
+  // the normaliser is an output of 32 bits: its logarithm, too, is one
+  const double lse = o.rs + static_cast<double>(__builtin_amdgcn_logf(static_cast<float>(o.ss)));
   const float nan = __builtin_nanf("");
   const float loss = o.bad ? nan : o.empty ? 0.0f : static_cast<float>(k * kLn2d);
   if ((threadIdx.x & 63) == 0) {
     out.kl[row] = loss;
-    out.lse[row] = o.bad ? nan : static_cast<float>(o.lse * kLn2d);
+    out.lse[row] = o.bad ? nan : static_cast<float>(lse * kLn2d);
     out.rest[row] = o.bad ? nan : static_cast<float>(rest2 * kLn2d);
     out.flags[row] = o.bad ? DSPARK_FLAG_NONFINITE : o.empty ? DSPARK_FLAG_EMPTY_ROW : 0;
   }
@@ -440,10 +442,9 @@ __device__ __forceinline__ void gran_store(T* g, const Row<T>& r, int q, bool ve
 // in flight at once cost bandwidth (14336 rows of 129280 bf16: 1342 us against
 // 1370 with 7); short rows want all.
 template <typename T, int NT, int ENT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 ? 8 : 5))) void distill_grad_kernel(const T* __restrict__ draft, DistillArgs a,
-                                                             const float* __restrict__ rest,
-                                                             const float* __restrict__ grad_scale, int64_t base,
-                                                             int32_t P, int32_t groups, T* __restrict__ grad) {
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 ? 8 : 5))) void distill_grad_kernel(
+    const T* __restrict__ draft, DistillArgs a, const float* __restrict__ rest, const float* __restrict__ grad_scale,
+    int64_t base, int32_t P, int32_t groups, T* __restrict__ grad) {
   constexpr int EPL = Row<T>::EPL, L = kL, TILE = NT * L;
   __shared__ __align__(16) int32_t sh_ids[64 * ENT];  // tokens to write over
   __shared__ float sh_d[64 * ENT];
@@ -474,9 +475,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 
       const double w = static_cast<double>(scale) * a.weight * (a.c64 / kLog2ed) *
                        exp(-static_cast<double>(row - b * a.gamma + 1) / a.gamma);
       zero = o.empty && !o.bad;
+      const double it = 1.0 / o.st, is = 1.0 / o.ss;
       double t[ENT];
 #pragma unroll
-      for (int i = 0; i < ENT; ++i) t[i] = e.id[i] >= 0 ? exp2(o.lt[i]) : 0.0;
+      for (int i = 0; i < ENT; ++i) t[i] = o.et[i] * it;
       if (o.twice) {
 #pragma unroll
         for (int i = 0; i < ENT; ++i) sh_t[i * 64 + lane] = t[i];
@@ -491,11 +493,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 
       const int32_t e0 = first * EPL - r.head, e1 = (first + groups * TILE) * EPL - r.head;  // of this segment
 #pragma unroll
       for (int i = 0; i < ENT; ++i) {
-        sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls[i]) - t[i]));
+        sh_d[i * 64 + lane] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (o.es[i] * is - t[i]));
         sh_ids[i * 64 + lane] = ((o.first >> i) & 1u) && e.id[i] >= e0 && e.id[i] < e1 ? e.id[i] : -1;
       }
       if (lane == 0) {
-        // the reference is rounded to fp32; what that loses goes into the factor
+        // the reference is rounded to fp32; what that loses (2^-lost, with |lost|
+        // under 2^-15 where a probability is not 0) goes into the factor
         float ref = static_cast<float>(rest2);
         double lost = rest2 - static_cast<double>(ref);
         const bool huge = fabsf(rst) >= kHugeLogit && rst != neg_inf();
@@ -506,7 +509,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 
           ref = 0.0f;
           lost = 0.0;
         }
-        shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (exp2(o.ls_r) - exp2(o.lt_r)) * exp2(-lost));
+        shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (o.es_r * is - o.et_r * it) * (1.0 - lost * kLn2d));
         shc[1] = ref;
         shf[1] = huge ? 1 : 0;
       }

@@ -198,6 +198,47 @@ __device__ __forceinline__ Mass group_mass(const uint4 (&u)[L], float c) {
   return Mass{m, s};
 }
 
+// 2^d in 64 bits for d <= 1 or so: Taylor's series of e^(f ln 2) on |f| <= 1/2,
+// whose first term left out, (ln 2 / 2)^12 / 12!, is under 2^-46.
+__device__ __forceinline__ double exp2_64(double d) {
+  d = fmax(d, -2000.0);
+  const double n = rint(d), x = (d - n) * 0.69314718055994530942;
+  double p = 1.0 / 39916800;
+  p = fma(p, x, 1.0 / 3628800);
+  p = fma(p, x, 1.0 / 362880);
+  p = fma(p, x, 1.0 / 40320);
+  p = fma(p, x, 1.0 / 5040);
+  p = fma(p, x, 1.0 / 720);
+  p = fma(p, x, 1.0 / 120);
+  p = fma(p, x, 1.0 / 24);
+  p = fma(p, x, 1.0 / 6);
+  p = fma(p, x, 0.5);
+  p = fma(p, x, 1.0);
+  p = fma(p, x, 1.0);
+  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+}
+
+// log2 of a normal x > 0 in 64 bits: x = 2^e m with m in [1/sqrt 2, sqrt 2], and
+// ln m = 2 artanh t, t = (m - 1) / (m + 1), |t| < 0.172: the series' first term
+// left out is under 2^-45 of it, so a logarithm near 0 keeps its relative accuracy.
+__device__ __forceinline__ double log2_64(double x) {
+  double m = __builtin_amdgcn_frexp_mant(x), e = static_cast<double>(__builtin_amdgcn_frexp_exp(x));
+  if (m < 0.70710678118654752440) {
+    m += m;
+    e -= 1.0;
+  }
+  const double t = (m - 1.0) / (m + 1.0), q = t * t;
+  double p = 1.0 / 15;
+  p = fma(p, q, 1.0 / 13);
+  p = fma(p, q, 1.0 / 11);
+  p = fma(p, q, 1.0 / 9);
+  p = fma(p, q, 1.0 / 7);
+  p = fma(p, q, 1.0 / 5);
+  p = fma(p, q, 1.0 / 3);
+  p = fma(p, q, 1.0);
+  return fma(p * t, 2.8853900817779268147, e);
+}
+
 // log2 of a mass, with c64 = log2(e) / T: the rounding of m c that s carries is
 // taken out again.  The terms are added in 64 bits; the logarithm of s is one
 // of 32 bits on its mantissa, off by less than 2^-23 (the sum itself is no better).

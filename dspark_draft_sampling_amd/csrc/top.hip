@@ -157,7 +157,7 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
       o.ids[row * K + rank] = key_index(k);
       top += __builtin_amdgcn_exp2f(mass_gap(x, wmax, c));
     } else {
-      sum += exp2((static_cast<double>(x) - static_cast<double>(wmax)) * c64);
+      sum += exp2_64((static_cast<double>(x) - static_cast<double>(wmax)) * c64);
     }
   }
   others = wave_mass(others, c);
@@ -203,7 +203,7 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
     }
   } else {
     const double ref = static_cast<double>(wmax);
-    const double lse = ref + log2(sum + exp2(mass_log2(others, c, c64) - ref * c64)) / c64;
+    const double lse = ref + log2_64(sum + exp2_64(mass_log2(others, c, c64) - ref * c64)) / c64;
     const double sc = static_cast<double>(bm.scores[row]);
     if (!bad)
       for (int i = tid; i < n; i += NT) {
