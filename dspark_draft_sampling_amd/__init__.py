@@ -22,6 +22,7 @@ from __future__ import annotations
 import atexit
 import ctypes as C
 import functools
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -677,44 +678,37 @@ def dspark_beam_reorder(state, parents, batch_dim=0, lengths=None, length_dim=No
     length_dim are moved.  Positions that are not moved, and rows whose parent is
     -1, keep what out holds (zeros where out is allocated here).  out=state
     reorders in place.  Returns out."""
-    if not isinstance(state, torch.Tensor):
-        raise DSparkError("beam_reorder: state must be a GPU tensor")
-    _dev_tensor(state, state.dtype, "state")
-    dev = state.device
+    if not isinstance(state, torch.Tensor) or not state.is_cuda or not state.is_contiguous():
+        raise DSparkError("beam_reorder: state must be a contiguous GPU tensor")
+    dev, size = state.device, state.shape
     d = int(batch_dim)
-    if d < 0 or d + 1 >= state.dim():
+    if d < 0 or d + 1 >= len(size):
         raise DSparkError("beam_reorder: batch_dim must name two dimensions of state")
-    _dev_tensor(parents, torch.int32, "parents", device=dev)
-    B, W = state.shape[d], state.shape[d + 1]
-    if parents.dim() != 2 or parents.shape[0] != B:
+    B, W = size[d], size[d + 1]
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise DSparkError("beam_reorder: parents must be [B, M]")
     M = parents.shape[1]
+    _want(parents, torch.int32, "parents", (B, M), dev)
     if (lengths is None) != (length_dim is None):
         raise DSparkError("beam_reorder: lengths and length_dim go together")
-    outer = inner = S = T = 1
-    for n in state.shape[:d]:
-        outer *= n
+    S = T = 1
     if lengths is None:
-        for n in state.shape[d + 2:]:
-            inner *= n
+        inner = math.prod(size[d + 2:])
     else:
-        _dev_tensor(lengths, torch.int32, "lengths", (B,), dev)
+        _want(lengths, torch.int32, "lengths", (B,), dev)
         t = int(length_dim)
-        if t < d + 2 or t >= state.dim():
+        if t < d + 2 or t >= len(size):
             raise DSparkError("beam_reorder: length_dim must be a dimension after the beams")
-        T = state.shape[t]
-        for n in state.shape[d + 2:t]:
-            S *= n
-        for n in state.shape[t + 1:]:
-            inner *= n
-    shape = (*state.shape[:d + 1], M, *state.shape[d + 2:])
+        S, T, inner = math.prod(size[d + 2:t]), size[t], math.prod(size[t + 1:])
+    outer = math.prod(size[:d])
+    shape = (*size[:d + 1], M, *size[d + 2:])
     if max(B, W, M, S, T) > 0x7fffffff:
         raise DSparkError("beam_reorder: a dimension is too large")
     with _on(dev) as c:
         if out is None:
             out = torch.zeros(shape, dtype=state.dtype, device=dev)
         else:
-            _dev_tensor(out, state.dtype, "out", shape, dev)
+            _want(out, state.dtype, "out", shape, dev)
         rc = lib().dspark_beam_reorder(_a(state), _a(out), _a(parents), _a(lengths), outer, B, W, M, S, T,
                                        inner * state.element_size(), c.stream)
     _check(rc)

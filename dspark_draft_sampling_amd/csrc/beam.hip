@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const char* 
   const int b = static_cast<int>(lb % B);
   int64_t t = T;
   if (lengths) t = min(max(lengths[b], 0), T);
-  const int64_t at = (chunk * kMoveThreads + threadIdx.x) * kU, left = t * token - at;
+  const int64_t at = (chunk * blockDim.x + threadIdx.x) * kU, left = t * token - at;
   if (left <= 0) return;
   const int64_t seg = static_cast<int64_t>(T) * token, row = seg * S;
   const char* from = src + lb * W * row + s * seg + at;
@@ -204,13 +204,15 @@ __global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const char* 
 template <typename U>
 hipError_t move(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L, int32_t B,
                 int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st) {
-  const int64_t chunks = (T * token / static_cast<int64_t>(sizeof(U)) + kMoveThreads - 1) / kMoveThreads;
+  const int64_t units = (T * token + static_cast<int64_t>(sizeof(U)) - 1) / static_cast<int64_t>(sizeof(U));
+  const int threads = units <= 64 ? 64 : kMoveThreads;  // of a run
+  const int64_t chunks = (units + threads - 1) / threads;
   const int64_t items = L * B * S * chunks;
   const bool in_place = src == dst;
   const char* s = static_cast<const char*>(src);
   char* d = static_cast<char*>(dst);
 #define DSPARK_MOVE(MB)                                                                                        \
-  DSPARK_LAUNCH("beam_reorder", (beam_reorder_kernel<U, MB>), grid, dim3(kMoveThreads), 0, st, s, d, parents, \
+  DSPARK_LAUNCH("beam_reorder", (beam_reorder_kernel<U, MB>), grid, dim3(threads), 0, st, s, d, parents, \
                 lengths, base, chunks, B, W, M, S, T, token, in_place)
   for (int64_t base = 0; base < items; base += kMaxGrid) {
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));

@@ -300,7 +300,7 @@ __global__ __launch_bounds__(NT, 4) void distill_loss_kernel(const T* __restrict
   if (wave_id() == 0) finish_row<ENT>(e, a, row, rest2, sh_ids, out);
 }
 
-// Row weights and sums.
+// Sums over the rows that count.
 struct Sums {
   double num, sum, cnt;
 };
@@ -309,10 +309,8 @@ struct Sums {
 __device__ __forceinline__ void position_weights(double* w, int32_t gamma) {
   if (threadIdx.x < DSPARK_MAX_GAMMA) w[threadIdx.x] = exp(-static_cast<double>(threadIdx.x + 1) / gamma);
 }
-__device__ __forceinline__ void add_row(Sums& s, const DistillArgs& a, const double* w, size_t row, float loss) {
-  const uint32_t r = static_cast<uint32_t>(row), b = r / static_cast<uint32_t>(a.gamma);
-  if (a.block_mask && !a.block_mask[b]) return;
-  s.num += w[r - b * a.gamma] * loss;
+__device__ __forceinline__ void add_row(Sums& s, double weight, float loss) {
+  s.num += weight * loss;
   s.sum += loss;
   s.cnt += 1.0;
 }
@@ -340,7 +338,9 @@ __global__ __launch_bounds__(kTinyThreads) void distill_tiny_kernel(const T* __r
     const Row<T> r = make_row(draft + row * a.V, a.V);
     const Entries<ENT> e = load_entries<T, ENT>(r, a, row);
     const double rest2 = outside_mass<T, 64, kTinyTiles>(r, a, row, lane, member[wave], nullptr);
-    add_row(s, a, shw, row, finish_row<ENT>(e, a, row, rest2, sh_ids[wave], out));
+    const float loss = finish_row<ENT>(e, a, row, rest2, sh_ids[wave], out);
+    const int b = rr / a.gamma;
+    if (!a.block_mask || a.block_mask[b]) add_row(s, shw[rr - b * a.gamma], loss);
   }
   if (lane == 0) shs[wave] = s;
   __syncthreads();
@@ -356,9 +356,11 @@ __global__ __launch_bounds__(kTinyThreads) void distill_tiny_kernel(const T* __r
 }
 
 // Sums of the rows' losses: a workgroup's stretch of rows, added in a fixed
-// order; several workgroups leave partial sums for distill_sums_final.
+// order; several workgroups leave partial sums for distill_sums_final.  magic:
+// ceil(2^36 / gamma), so that row / gamma = row magic >> 36 for every row < 2^31
+// (row (magic gamma - 2^36) < 2^31 16 < 2^36).
 __global__ __launch_bounds__(kSumThreads) void distill_sums_kernel(const float* __restrict__ kl, DistillArgs a,
-                                                                   int32_t R, int32_t stretch,
+                                                                   int32_t R, int32_t stretch, uint64_t magic,
                                                                    Sums* __restrict__ partial,
                                                                    float* __restrict__ sums) {
   __shared__ Sums shs[kSumThreads / 64];
@@ -369,8 +371,25 @@ __global__ __launch_bounds__(kSumThreads) void distill_sums_kernel(const float* 
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * stretch;
   const int64_t r1 = min(r0 + stretch, static_cast<int64_t>(R));
   Sums s{0.0, 0.0, 0.0};
-  for (int64_t row = r0 + threadIdx.x; row < r1; row += kSumThreads)
-    add_row(s, a, shw, static_cast<size_t>(row), kl[row]);
+  // without a mask a byte of kl is read in its place, so that no branch parts the loads
+  const uint8_t* mask = a.block_mask ? a.block_mask : reinterpret_cast<const uint8_t*>(kl);
+  constexpr int U = 8;  // rows whose loads are in flight together
+  for (int64_t row = r0 + threadIdx.x; row < r1; row += U * kSumThreads) {
+    float v[U];
+    uint32_t k[U];
+    bool on[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t q = min(row + i * kSumThreads, r1 - 1);
+      const uint32_t b = static_cast<uint32_t>((static_cast<uint64_t>(q) * magic) >> 36);
+      k[i] = static_cast<uint32_t>(q) - b * static_cast<uint32_t>(a.gamma);
+      v[i] = kl[q];
+      on[i] = mask[a.block_mask ? b : 0u] != 0 || !a.block_mask;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (on[i] && row + i * kSumThreads < r1) add_row(s, shw[k[i]], v[i]);
+  }
   s = Sums{wave_sum64(s.num), wave_sum64(s.sum), wave_sum64(s.cnt)};
   if (lane == 0) shs[wave] = s;
   __syncthreads();
@@ -582,8 +601,9 @@ hipError_t launch_loss(const T* draft, const DistillArgs& a, int32_t R, const Lo
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int blocks = std::min(kMaxSumBlocks, (R + 16383) / 16384);
+  const uint64_t magic = ((1ull << 36) + a.gamma - 1) / a.gamma;
   DSPARK_LAUNCH("distill_sums", distill_sums_kernel, dim3(blocks), dim3(kSumThreads), 0, st, out.kl, a, R,
-                (R + blocks - 1) / blocks, partial, sums);
+                (R + blocks - 1) / blocks, magic, partial, sums);
   if (blocks > 1)
     DSPARK_LAUNCH("distill_sums_final", distill_sums_final_kernel, dim3(1), dim3(64), 0, st, partial, blocks, a.weight,
                   sums);

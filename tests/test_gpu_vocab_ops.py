@@ -166,6 +166,51 @@ def test_top_logits_shapes():
     assert empty["top_ids"].shape == (0, 5)
 
 
+@pytest.mark.parametrize("dtype,R,V,K", [("bf16", 2100, 9000, 9), ("bf16", 2100, 30011, 32), ("f32", 2100, 5003, 30),
+                                         ("bf16", 2100, 9000, 40), ("f32", 600, 129280, 20), ("bf16", 600, 140001, 33)])
+def test_top_logits_every_way_to_take_a_row(dtype, R, V, K):
+    # a wave a row, workgroups of 256, rows in several segments: rows alone (few) and in a batch (many)
+    g = torch.Generator(device=G.DEV).manual_seed(V)
+    x = (torch.randn(R, V, generator=g, device=G.DEV) * 3).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    got = host(ds.dspark_top_logits(x, K))
+    for r in (0, 1, R // 2, R - 1):
+        one = check_top(x[r:r + 1].float().cpu().numpy(), dtype, K)
+        for k in ("top_values", "top_ids", "flags"):
+            assert np.array_equal(got[k][r], one[k][0])
+        for k in ("rest", "lse"):
+            assert ref.near(got[k][r], np.float64(one[k][0]), 2 * ref.MASS_TOL)
+
+
+def test_more_rows_than_a_grid_takes():
+    """Counts past the 2^22 workgroups of one launch."""
+    R = (1 << 22) + 5
+    x = torch.randint(-8, 8, (R, 3), device=G.DEV).to(torch.float32)
+    got = ds.dspark_top_logits(x, 2)
+    v, i = torch.sort(x, dim=-1, descending=True, stable=True)
+    assert torch.equal(got["top_values"], v[:, :2]) and torch.equal(got["top_ids"].long(), i[:, :2])
+    N, g = 300_000, 16
+    d = torch.randn(N, g, 4, device=G.DEV)
+    top = ds.dspark_top_logits(torch.randn(N, g, 4, device=G.DEV), 2)
+    a = (top["top_values"], top["top_ids"])
+    loss = ds.dspark_distill(d, *a, teacher_rest=top["rest"])
+    grad = ds.dspark_distill_backward(d, *a, loss["rest"], teacher_rest=top["rest"])["grad_draft"]
+    n = slice(N - 3, N)
+    part = ds.dspark_distill(d[n].clone(), a[0][n].clone(), a[1][n].clone(), teacher_rest=top["rest"][n].clone())
+    pg = ds.dspark_distill_backward(d[n].clone(), a[0][n].clone(), a[1][n].clone(), part["rest"],
+                                    teacher_rest=top["rest"][n].clone())["grad_draft"]
+    assert torch.equal(loss["kl"][n], part["kl"]) and torch.equal(grad[n], pg)
+    w = torch.exp(-torch.arange(1, g + 1, device=G.DEV).double() / g)
+    # the losses as written are the summands: only the 64-bit sums' rounding is between
+    assert ref.near(float(loss["sums"][0]), float((loss["kl"].double() * w).sum()), 1e-3)
+    assert float(loss["sums"][3]) == N * g
+    B = (1 << 22) + 3
+    pick = ds.dspark_beam_select(torch.randint(-8, 8, (B, 1, 2), device=G.DEV).float(), torch.zeros(B, 1, device=G.DEV), 2)
+    assert torch.all(pick["tokens"].sum(1) == 1) and not pick["parents"].any()
+    state = torch.arange(2 * B, device=G.DEV, dtype=torch.int32).view(B, 2)
+    swap = torch.tensor([[1, 0]], dtype=torch.int32, device=G.DEV).expand(B, 2).contiguous()
+    assert torch.equal(ds.dspark_beam_reorder(state, swap), state.flip(1))
+
+
 def test_top_logits_past_32_bit_offsets():
     V, R = 129280, 16700  # R V passes 2^31 elements
     x = torch.zeros((R, V), dtype=torch.bfloat16, device=G.DEV)
