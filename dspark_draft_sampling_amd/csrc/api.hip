@@ -8,6 +8,7 @@
 
 #include "dspark.h"
 #include "internal.hpp"
+#include "vocab.hpp"
 
 namespace {
 

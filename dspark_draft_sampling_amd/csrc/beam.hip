@@ -19,8 +19,8 @@
 #include <algorithm>
 
 #include "common.hpp"
-#include "internal.hpp"
 #include "rowstream.hpp"
+#include "vocab.hpp"
 
 namespace dspark {
 namespace {

@@ -25,8 +25,8 @@
 #include <algorithm>
 
 #include "common.hpp"
-#include "internal.hpp"
 #include "rowstream.hpp"
+#include "vocab.hpp"
 
 namespace dspark {
 namespace {
