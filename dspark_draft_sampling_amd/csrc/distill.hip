@@ -36,7 +36,7 @@ constexpr int kL = 4;              // granules of a group
 constexpr int kMaxTiles = 16;      // groups of a thread whose mask words are held at a time
 constexpr int kTinyThreads = 1024; // one-launch form: a wave a row
 constexpr int kTinyWaves = kTinyThreads / 64;
-constexpr int kTinyTiles = 4;
+constexpr int kTinyTiles = 2;
 constexpr int kSumThreads = 1024;
 constexpr int kMaxSumBlocks = 64;
 constexpr double kLn2d = 0.69314718055994530942;
@@ -528,7 +528,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4, NT == 64 
           ref = 0.0f;
           lost = 0.0;
         }
-        shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(w * (o.es_r * is - o.et_r * it) * (1.0 - lost * kLn2d));
+        const double f = w * (o.es_r * is - o.et_r * it) * (1.0 - lost * kLn2d);
+        shc[0] = o.bad ? __builtin_nanf("") : static_cast<float>(f);
         shc[1] = ref;
         shf[1] = huge ? 1 : 0;
       }
@@ -583,17 +584,26 @@ hipError_t launch_loss(const T* draft, const DistillArgs& a, int32_t R, const Lo
                        hipStream_t st) {
   constexpr int L = kL;
   const int q = row_granules(Row<T>::EPL, a.V);
-  if (R <= 64 && q <= kTinyTiles * 64 * L) {
+  // One launch where the rows are hardly more than a workgroup's waves (V = 1024
+  // fp32: 16 rows 7.2 us against 8.9 of two launches, 24 rows 9.3 against 9.1 but a
+  // launch less, 32 rows 13.5 against 8.8).
+  if (R <= kTinyWaves + kTinyWaves / 2 && q <= kTinyTiles * 64 * L) {
     DSPARK_LAUNCH("distill_tiny", (distill_tiny_kernel<T, ENT>), dim3(1), dim3(kTinyThreads), 0, st, draft, a, R, out,
                   sums);
     return hipGetLastError();
   }
+  // A wave a row where rows are short, or many and not long (16000 rows of 16000
+  // bf16: 108 us against 121 of 256 threads; 8000 of 1500: 23 against 46); 512
+  // threads where rows are few and long (256 rows of 129280: 23 us against 29 of 256
+  // threads; 1024 rows: 55 against 53).
+  const bool wave = q <= 2 * 64 * L || (R >= 4096 && q <= kMaxTiles * 64 * L);
+  const int nt = wave ? 64 : R > 512 || q <= 2 * 256 * L ? 256 : 512;
   for (int32_t base = 0, n; base < R; base += n) {
     n = std::min(R - base, kMaxGrid);
     const dim3 grid(static_cast<unsigned>(n));
-    if (q <= 2 * 64 * L)
+    if (nt == 64)
       DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 64, ENT>), grid, dim3(64), 0, st, draft, a, base, out);
-    else if (R > 512 || q <= 4 * 256 * L)
+    else if (nt == 256)
       DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 256, ENT>), grid, dim3(256), 0, st, draft, a, base, out);
     else
       DSPARK_LAUNCH("distill_loss", (distill_loss_kernel<T, 512, ENT>), grid, dim3(512), 0, st, draft, a, base, out);
@@ -615,9 +625,13 @@ hipError_t launch_grad(const T* draft, const DistillArgs& a, int32_t R, const fl
                        T* grad, hipStream_t st) {
   constexpr int L = kL;
   const int q = row_granules(Row<T>::EPL, a.V);
+  // a wave a row where rows are short (8000 rows of 4000 bf16: 28 us against 37 of
+  // 256 threads; of 8000: 59 against 55)
   const int nt = q <= 2 * 64 * L ? 64 : 256;
   const int need = (q + nt * L - 1) / (nt * L);  // groups of a thread over the row
-  int groups = need;  // shorter segments where that fills the GPU
+  // shorter segments where that fills the GPU (128 rows of 129280 bf16: 14 us with 8
+  // segments a row, 24 with one)
+  int groups = need;
   while (groups > 1 && static_cast<int64_t>(R) * ((need + groups - 1) / groups) < 512) groups = (groups + 1) / 2;
   const int P = (need + groups - 1) / groups;
   const int64_t items = static_cast<int64_t>(R) * P;

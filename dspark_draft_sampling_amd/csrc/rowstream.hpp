@@ -361,7 +361,8 @@ __device__ __forceinline__ Count3 block_count(Count3 n, uint64_t* slots, int& st
   } else {
     uint64_t* s = slots + (step++ & 1) * NW;
     if ((threadIdx.x & 63) == 0)
-      s[threadIdx.x >> 6] = static_cast<uint64_t>(n.a) | static_cast<uint64_t>(n.b) << 21 | static_cast<uint64_t>(n.c) << 42;
+      s[threadIdx.x >> 6] = static_cast<uint64_t>(n.a) | static_cast<uint64_t>(n.b) << 21 |
+                            static_cast<uint64_t>(n.c) << 42;
     __syncthreads();
     uint64_t t = 0;
 #pragma unroll

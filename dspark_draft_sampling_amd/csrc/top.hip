@@ -142,7 +142,7 @@ __device__ __forceinline__ void write_best(uint64_t* list, int n, int nv, int K,
   for (int i = tid; i < n; i += NT) {
     const uint64_t k = list[i];
     int rank = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < n; j += 4) {
       const uint64_t k0 = list[j], k1 = list[j + 1], k2 = list[j + 2], k3 = list[j + 3];
       rank += (k0 > k) + (k1 > k) + (k2 > k) + (k3 > k);
@@ -277,7 +277,8 @@ __device__ __forceinline__ int exact_candidates(const Row<T>& r, int q0, int q1,
     return v;
   };
   int n_lo = INT32_MAX;
-  const uint32_t t = search_key<uint32_t>(kKeyNegInf + 1, kmax + 1, n_lo, K, K, [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+  const uint32_t t = search_key<uint32_t>(kKeyNegInf + 1, kmax + 1, n_lo, K, K, [&](uint32_t t1, uint32_t t2,
+                                                                                    uint32_t t3) {
     Count3 n{0, 0, 0};
     for (int q = q0 + tid; q < q1; q += NT) {
       const uint4 u = gran_load(r, q);
@@ -419,8 +420,11 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
       }
       if (nb > K)
         bound = search_key<uint32_t>(bound, kmax + 1, nb, K, list_len(K), [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-          return block_count<NW>(Count3{static_cast<int>(__popcll(__ballot(k >= t1))), static_cast<int>(__popcll(__ballot(k >= t2))),
-                                        static_cast<int>(__popcll(__ballot(k >= t3)))}, s.slots, step);
+          Count3 w{0, 0, 0};
+          w.a = __popcll(__ballot(k >= t1));
+          w.b = __popcll(__ballot(k >= t2));
+          w.c = __popcll(__ballot(k >= t3));
+          return block_count<NW>(w, s.slots, step);
         });
     } else {
       auto groups_at = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
@@ -549,8 +553,8 @@ __global__ __launch_bounds__(NT, 4) void top_segment_kernel(const T* __restrict_
 constexpr int kSmallCand = TopCaps<64>::kRank;
 
 template <typename T, int L, TopMode MODE>
-__global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ logits, int32_t base, int32_t V, int32_t K,
-                                                       float c, double c64, TopBeams bm, TopOut o) {
+__global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ logits, int32_t base, int32_t V,
+                                                          int32_t K, float c, double c64, TopBeams bm, TopOut o) {
   constexpr int EPL = Row<T>::EPL;
   __shared__ uint64_t cand[kSmallCand + 4];
   __shared__ RankLds<64> out;
@@ -646,8 +650,8 @@ __global__ __launch_bounds__(64, 4) void top_small_kernel(const T* __restrict__ 
 // workgroup a row; kRows or kBeams.
 template <TopMode MODE>
 __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t* __restrict__ in,
-                                                                  const Mass* __restrict__ parts, int32_t base, int32_t K,
-                                                                  int32_t P, float c, double c64, TopBeams bm,
+                                                                  const Mass* __restrict__ parts, int32_t base,
+                                                                  int32_t K, int32_t P, float c, double c64, TopBeams bm,
                                                                   TopOut o) {
   constexpr int NT = kMergeThreads, NW = NT / 64;
   extern __shared__ uint64_t all[];  // P list_len(K) keys and 4 more
@@ -712,7 +716,21 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
 }
 
 // Rows are cut into segments of `groups` groups a thread; groups = 0: short rows,
-// NT granules a lane of one wave.
+// NT granules a lane of one wave.  Measured, one side against the other:
+//  * a row in one wave's registers, up to 512 granules: 400000 rows of 1500 bf16, K =
+//    20, 532 us against 974 of the segment kernel with one wave a row (K = 100 and
+//    100000 rows of 3500: 415 against 1150 with 256 threads);
+//  * one wave a row where rows are many, of up to 16 groups for K <= 32, whose bound
+//    comes from 64 threads' maxima (3000 rows of 20000 bf16, K = 20: 31 us against 42
+//    of 256 threads), of up to 4 for larger K, whose bound comes from the groups'
+//    (20000 rows of 8000, K = 100: 193 against 226; 5000 of 20000, K = 64: 87
+//    against 75);
+//  * 512 threads for few long rows: 256 rows of 129280 bf16 17.7 us against 21.3 of 256
+//    threads; 700 rows 49 against 43 (several workgroups of 256 share a compute unit,
+//    and one's tail runs beside the others' streams);
+//  * several segments a row only where one cannot hold it: the merge is a launch
+//    more (64 rows of 129280: 17 us against 16 with one; one row: 13 against 15, less
+//    than the second launch costs the host).
 TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
   // granules of a row, at the least favourable alignment
   const int q = any ? (V + 2 * epl - 2) / epl : V / epl;
@@ -723,7 +741,7 @@ TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
     return s;
   }
   int most, kL = 4;
-  if (q <= TopCaps<64>::kG * 64 * kL && R >= 2048 && K <= 32) {
+  if (R >= 2048 && q <= (K <= 32 ? TopCaps<64>::kG : 4) * 64 * kL) {
     s.NT = 64;
     most = TopCaps<64>::kG;
   } else if (q > 4 * 256 * kL && R <= 512) {
@@ -747,7 +765,7 @@ template <typename T, TopMode MODE>
 hipError_t launch_segments(const T* logits, int32_t R, int32_t V, int32_t K, const TopSplit& sp, float c, double c64,
                            const TopBeams& bm, const TopOut& o, hipStream_t st) {
   const int64_t items = static_cast<int64_t>(R) * sp.P;
-#define DSPARK_TOP(NT, L)                                                                                               \
+#define DSPARK_TOP(NT, L) \
   DSPARK_LAUNCH("top_segment", (top_segment_kernel<T, NT, L, MODE>), grid, dim3(NT), 0, st, logits, base, V, K, sp.P, \
                 sp.groups, c, c64, bm, o)
   for (int64_t base = 0; base < items; base += kMaxGrid) {
@@ -821,8 +839,8 @@ bool any_alignment(const void* p, int32_t V, int epl) {
 
 }  // namespace
 
-float mass_scale(float temperature) { return static_cast<float>(1.4426950408889634074 / static_cast<double>(temperature)); }
 double mass_scale64(float temperature) { return 1.4426950408889634074 / static_cast<double>(temperature); }
+float mass_scale(float temperature) { return static_cast<float>(mass_scale64(temperature)); }
 
 // Sized for either type and any alignment of the rows.
 TopPlan plan_top(int32_t R, int32_t V, int32_t K) {
