@@ -4,6 +4,8 @@ selection and reordering) on the GPU against their 64-bit forms
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import pytest
 
@@ -209,6 +211,25 @@ def test_more_rows_than_a_grid_takes():
     state = torch.arange(2 * B, device=G.DEV, dtype=torch.int32).view(B, 2)
     swap = torch.tensor([[1, 0]], dtype=torch.int32, device=G.DEV).expand(B, 2).contiguous()
     assert torch.equal(ds.dspark_beam_reorder(state, swap), state.flip(1))
+
+
+def test_distill_sums_past_2_to_the_28_rows():
+    N = (1 << 28) + 5
+    d = torch.zeros(N, 1, 2, dtype=torch.bfloat16, device=G.DEV)
+    v = torch.zeros(N, 1, 1, device=G.DEV)
+    i = torch.zeros(N, 1, 1, dtype=torch.int32, device=G.DEV)
+    mask = torch.zeros(N, dtype=torch.uint8, device=G.DEV)
+    on = [7, N - 3, N - 1]
+    for n in on:
+        mask[n] = 1
+        d[n, 0, 1] = 1.0
+    got = ds.dspark_distill(d, v, i, block_mask=mask)
+    kl = [float(got["kl"][n, 0]) for n in on]
+    # the losses as written are the summands; one rounding of the sum to 32 bits
+    assert ref.near(float(got["sums"][0]), math.exp(-1.0) * sum(kl), 2.0 ** -23)
+    assert ref.near(float(got["sums"][2]), sum(kl), 2.0 ** -23)
+    assert float(got["sums"][1]) == float(got["sums"][3]) == len(on)
+    assert all(abs(k - math.log(1 + math.e)) < 1e-5 for k in kl)
 
 
 def test_top_logits_past_32_bit_offsets():
