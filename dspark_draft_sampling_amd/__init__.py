@@ -24,6 +24,7 @@ import ctypes as C
 import functools
 import math
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -506,7 +507,8 @@ class _on:
 
     def scratch(self, op, *sizes):
         """(address, bytes) of the call's workspace.  Outside a stream capture
-        it is the cached one of (device, stream, op).  A captured call gets memory
+        it is the cached one of (device, stream, op, thread): the launches of two
+        threads' calls on one stream may alternate.  A captured call gets memory
         of its graph's own pool: a graph keeps using the address, so a buffer that
         eager calls share and may replace by a larger one would not do, nor one
         that two graphs share."""
@@ -516,9 +518,10 @@ class _on:
         if torch.cuda.is_current_stream_capturing():
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             return ws.data_ptr(), nbytes
-        ws = _ws.get((self.device, self.stream, op))
+        which = (op, threading.get_ident())
+        ws = _ws.get((self.device, self.stream, which))
         if ws is None or ws.numel() < nbytes:
-            ws = _workspace(op, self.device, nbytes)
+            ws = _workspace(which, self.device, nbytes)
         return ws.data_ptr(), ws.numel()
 
 

@@ -5,6 +5,7 @@ selection and reordering) on the GPU against their 64-bit forms
 from __future__ import annotations
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -723,3 +724,28 @@ def test_two_streams_at_once():
         got = host(o)
         for k in got:
             assert np.array_equal(got[k], refs[n % 2][k], equal_nan=True), (n, k)
+
+
+def test_two_threads_on_one_stream():
+    ins = [(torch.randn(3, 4, 20000 + n, device=G.DEV), torch.randn(3, 4, device=G.DEV), 8 + n) for n in range(2)]
+    refs = [host(ds.dspark_beam_select(*i)) for i in ins]
+    outs = [[] for _ in ins]
+    start = threading.Barrier(len(ins))
+
+    def work(n):
+        start.wait()
+        for _ in range(200):
+            outs[n].append(ds.dspark_beam_select(*ins[n]))
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(len(ins))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for n, results in enumerate(outs):
+        assert len(results) == 200
+        for o in results:
+            got = host(o)
+            for k in got:
+                assert np.array_equal(got[k], refs[n][k]), (n, k)
