@@ -557,8 +557,8 @@ def dspark_top_logits(logits, k, temperature=1.0, out=None):
         raise DSparkError("top_logits: logits must be [..., V]")
     *lead, V = logits.shape
     k = int(k)
-    if k < 0:
-        raise DSparkError("top_logits: k must be positive")
+    if not 0 <= k <= DSPARK_MAX_TOP:
+        raise DSparkError(f"top_logits: k must be in [1, {DSPARK_MAX_TOP}]")
     R = 1
     for n in lead:
         R *= n
@@ -585,6 +585,8 @@ def _distill_args(what, draft, values, ids, teacher_rest, block_mask):
     if draft.dim() != 3:
         raise DSparkError(f"{what}: draft must be [N, gamma, V]")
     N, g, V = draft.shape
+    if max(N, g, V) > 0x7fffffff:
+        raise DSparkError(f"{what}: a dimension of draft is too large")
     dev = draft.device
     if not isinstance(values, torch.Tensor) or values.dim() != 3:
         raise DSparkError(f"{what}: teacher_values must be [N, gamma, K]")
@@ -654,19 +656,25 @@ def dspark_beam_select(logits, scores, picks, finished=None, eos_token=0, out=No
     if logits.dim() != 3:
         raise DSparkError("beam_select: logits must be [B, W, V]")
     B, W, V = logits.shape
-    M = int(picks)
-    if M < 0:
-        raise DSparkError("beam_select: picks must be positive")
+    M, eos = int(picks), int(eos_token)
+    if max(B, W, V) > 0x7fffffff:
+        raise DSparkError("beam_select: a dimension of logits is too large")
+    if not 0 <= M <= DSPARK_MAX_TOP:
+        raise DSparkError(f"beam_select: picks must be in [1, {DSPARK_MAX_TOP}]")
     dev = logits.device
     _want(scores, torch.float32, "scores", (B, W), dev)
-    if finished is not None:
+    if finished is None:
+        eos = 0  # not read
+    else:
         _want(finished, torch.uint8, "finished", (B, W), dev)
+        if not 0 <= eos < V:
+            raise DSparkError("beam_select: eos_token must be a token")
     with _on(dev) as c:
         out = _outputs("beam_select", [("tokens", torch.int32, (B, M)), ("parents", torch.int32, (B, M)),
                                        ("scores", torch.float32, (B, M)), ("flags", torch.uint8, (B, W))],
                        out, dev)
         ws, nb = c.scratch(DSPARK_OP_BEAM, B, W, V, M)
-        rc = lib().dspark_beam_select(_a(logits), dt, _a(scores), _a(finished), int(eos_token), B, W, V, M,
+        rc = lib().dspark_beam_select(_a(logits), dt, _a(scores), _a(finished), eos, B, W, V, M,
                                       _a(out["tokens"]), _a(out["parents"]), _a(out["scores"]),
                                       _a(out["flags"]), ws, nb, c.stream)
     _check(rc)

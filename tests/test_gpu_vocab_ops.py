@@ -596,6 +596,28 @@ def test_bindings_refuse_bad_arguments():
     torch.cuda.synchronize()
 
 
+def test_bindings_refuse_what_32_bits_would_cut():
+    """Numbers whose lower 32 bits would be valid."""
+    x = torch.zeros(2, 3, 40, device=G.DEV)
+    sc = torch.zeros(2, 3, device=G.DEV)
+    done = torch.zeros(2, 3, dtype=torch.uint8, device=G.DEV)
+    wide = torch.empty(1, 1, (1 << 32) + 8, dtype=torch.bfloat16, device=G.DEV)
+    one = torch.zeros(1, 1, 1, device=G.DEV)
+    calls = [
+        lambda: ds.dspark_top_logits(x, (1 << 32) + 4), lambda: ds.dspark_beam_select(x, sc, (1 << 32) + 4),
+        lambda: ds.dspark_beam_select(x, sc, 2, finished=done, eos_token=(1 << 32) + 1),
+        lambda: ds.dspark_beam_select(x, sc, 2, finished=done, eos_token=-1),
+        lambda: ds.dspark_top_logits(wide, 4), lambda: ds.dspark_beam_select(wide, one[0], 2),
+        lambda: ds.dspark_distill(wide, one, one.int()), lambda: ds.dspark_distill_backward(wide, one, one.int(), one[0]),
+    ]
+    for n, call in enumerate(calls):
+        with pytest.raises(ds.DSparkError):
+            call()
+            pytest.fail(f"call {n} was not refused")
+    ds.dspark_beam_select(x, sc, 2, eos_token=-1)  # not read without finished
+    torch.cuda.synchronize()
+
+
 # ---- together -----------------------------------------------------------------------
 
 
