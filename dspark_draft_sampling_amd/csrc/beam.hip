@@ -31,6 +31,8 @@ constexpr int kMaxCand = DSPARK_MAX_BEAMS * DSPARK_MAX_TOP;
 constexpr int kRankAll = 64;  // candidates ranked at once; more are first cut by a search (128: 7 us against 4.6)
 constexpr int kMaxGrid = 1 << 22;  // workgroups of a launch; more are further launches
 
+// W M candidates a request: a chain of a few barriers, 3.4 us for 32 candidates, 4.6
+// for 256, of which 3 are any launch's.
 __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_t* __restrict__ sums,
                                                                    const uint64_t* __restrict__ keys, int32_t base,
                                                                    int32_t W, int32_t M,
