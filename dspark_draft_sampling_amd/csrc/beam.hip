@@ -136,31 +136,62 @@ __global__ __launch_bounds__(kFinalThreads) void beam_final_kernel(const uint64_
 
 // ---- reordering -------------------------------------------------------------------
 // A row of a beam is S runs of T tokens; only the tokens before the request's
-// length move.  Runs that are multiples of 16 bytes at 16-byte addresses move in
-// 16-byte units, the last bytes of a length singly; others in the widest of 4, 2
-// and 1 bytes that divides token and address.  One workgroup moves a stretch of
-// units of one run of every beam of a request: MB children at a time, all of them
-// loaded before any is stored (in place: MB >= M).  16-byte stores are
-// non-temporal (1.6 GB of caches: 508 us, 5.7 TB/s, against 563; non-temporal
-// loads slow it down: a parent's children then read it again).
+// length move, in units of 16 bytes at any address.  A run's last unit ends with
+// it; in place, and in runs of less than a unit, its last bytes move as 8, 4, 2 and
+// 1.  One workgroup moves a stretch of units of one run of every beam of a request:
+// MB children at a time, all of them loaded before any is stored (in place: MB >=
+// M).  Bound by HBM: 1.6 GB of caches 505 us, 5.7 TB/s, a parent with several
+// children read once.  Units that fit token and address took 58 us for 50 MB of
+// 1023 tokens of 6 bytes a run where these take 18, and 147 for 201 MB of tokens of
+// 12 against 53; aligned runs are no slower.  The stores of 16 bytes are
+// non-temporal (563 us without; non-temporal loads, 606: a parent's children read
+// it again).
 constexpr int kMoveThreads = 256;
+constexpr int64_t kUnit = 16;
+constexpr int32_t kNotInPlace = 1 << 30;  // above every parent
 
-template <typename U>
-__device__ __forceinline__ void put(U* p, U v) {
-  if constexpr (sizeof(U) == 16)
-    __builtin_nontemporal_store(v, p);
-  else
-    *p = v;
+// Units at any address: vector memory instructions take unaligned ones.
+struct Unit16 {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(1)));
+};
+struct Unit8 {
+  typedef uint64_t type __attribute__((aligned(1)));
+};
+struct Unit4 {
+  typedef uint32_t type __attribute__((aligned(1)));
+};
+struct Unit2 {
+  typedef uint16_t type __attribute__((aligned(1)));
+};
+struct Unit1 {
+  typedef uint8_t type;
+};
+
+// One unit of the children j0 + [0, MB) of the parents p (-1: none; beam 0 is read
+// in its place, so that no branch parts the loads).
+template <typename U, int MB>
+__device__ __forceinline__ void move_unit(const char* from, char* to, int64_t row, int j0, const int (&p)[MB]) {
+  typename U::type v[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) v[j] = *reinterpret_cast<const typename U::type*>(from + max(p[j], 0) * row);
+#pragma unroll
+  for (int j = 0; j < MB; ++j)
+    if (p[j] >= 0) {
+      typename U::type* a = reinterpret_cast<typename U::type*>(to + (j0 + j) * row);
+      if constexpr (sizeof(*a) == 16)
+        __builtin_nontemporal_store(v[j], a);
+      else
+        *a = v[j];
+    }
 }
 
-template <typename U, int MB>
+template <int MB>
 __global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const char* src, char* dst,
                                                                     const int32_t* __restrict__ parents,
                                                                     const int32_t* __restrict__ lengths, int64_t base,
                                                                     int64_t chunks, int32_t B, int32_t W, int32_t M,
                                                                     int32_t S, int32_t T, int64_t token,
-                                                                    bool in_place) {
-  constexpr int64_t kU = sizeof(U);
+                                                                    int32_t own) {
   const int64_t item = base + blockIdx.x;
   const int64_t run = item / chunks, chunk = item - run * chunks;
   const int64_t lb = run / S;
@@ -168,67 +199,37 @@ __global__ __launch_bounds__(kMoveThreads) void beam_reorder_kernel(const char* 
   const int b = static_cast<int>(lb % B);
   int64_t t = T;
   if (lengths) t = min(max(lengths[b], 0), T);
-  const int64_t at = (chunk * blockDim.x + threadIdx.x) * kU, left = t * token - at;
+  int64_t at = (chunk * blockDim.x + threadIdx.x) * kUnit, left = t * token - at;
   if (left <= 0) return;
+  if (left < kUnit && at > 0 && own == kNotInPlace) {
+    at -= kUnit - left;  // part of it is moved twice, from a source that does not change
+    left = kUnit;
+  }
   const int64_t seg = static_cast<int64_t>(T) * token, row = seg * S;
   const char* from = src + lb * W * row + s * seg + at;
   char* to = dst + lb * M * row + s * seg + at;
+#pragma unroll 1
   for (int j0 = 0; j0 < M; j0 += MB) {
-    int p[MB];
+    int p[MB], some = -1;
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
       p[j] = -1;
       if (j0 + j < M) p[j] = parents[static_cast<int64_t>(b) * M + j0 + j];
-      if (p[j] >= W || (in_place && p[j] == j0 + j)) p[j] = -1;
+      p[j] = __builtin_amdgcn_readfirstlane(p[j]);  // the same for the workgroup: scalar addresses and branches
+      if (p[j] >= W || p[j] == own + j0 + j) p[j] = -1;
+      some = max(some, p[j]);
     }
-    if (left >= kU) {
-      U v[MB];
-#pragma unroll
-      for (int j = 0; j < MB; ++j)
-        if (p[j] >= 0) v[j] = *reinterpret_cast<const U*>(from + p[j] * row);
-#pragma unroll
-      for (int j = 0; j < MB; ++j)
-        if (p[j] >= 0) put(reinterpret_cast<U*>(to + (j0 + j) * row), v[j]);
+    if (some < 0) continue;
+    if (left >= kUnit) {
+      move_unit<Unit16, MB>(from, to, row, j0, p);
     } else {
-      for (int64_t i = 0; i < left; ++i) {
-        char v[MB];
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-          if (p[j] >= 0) v[j] = from[p[j] * row + i];
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-          if (p[j] >= 0) to[(j0 + j) * row + i] = v[j];
-      }
+      const int l4 = static_cast<int>(left) & 8, l2 = static_cast<int>(left) & 12, l1 = static_cast<int>(left) & 14;
+      if (left & 8) move_unit<Unit8, MB>(from, to, row, j0, p);
+      if (left & 4) move_unit<Unit4, MB>(from + l4, to + l4, row, j0, p);
+      if (left & 2) move_unit<Unit2, MB>(from + l2, to + l2, row, j0, p);
+      if (left & 1) move_unit<Unit1, MB>(from + l1, to + l1, row, j0, p);
     }
   }
-}
-
-template <typename U>
-hipError_t move(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L, int32_t B,
-                int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st) {
-  const int64_t units = (T * token + static_cast<int64_t>(sizeof(U)) - 1) / static_cast<int64_t>(sizeof(U));
-  const int threads = units <= 64 ? 64 : kMoveThreads;  // of a run
-  const int64_t chunks = (units + threads - 1) / threads;
-  const int64_t items = L * B * S * chunks;
-  const bool in_place = src == dst;
-  const char* s = static_cast<const char*>(src);
-  char* d = static_cast<char*>(dst);
-#define DSPARK_MOVE(MB)                                                                                        \
-  DSPARK_LAUNCH("beam_reorder", (beam_reorder_kernel<U, MB>), grid, dim3(threads), 0, st, s, d, parents, \
-                lengths, base, chunks, B, W, M, S, T, token, in_place)
-  for (int64_t base = 0; base < items; base += kMaxGrid) {
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));
-    if (M <= 4)
-      DSPARK_MOVE(4);
-    else if (M <= 8 || !in_place)
-      DSPARK_MOVE(8);
-    else if (M <= 16)
-      DSPARK_MOVE(16);
-    else
-      DSPARK_MOVE(32);
-  }
-#undef DSPARK_MOVE
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -267,12 +268,29 @@ hipError_t launch_beam_select(const void* logits, int dtype, const float* scores
 
 hipError_t launch_beam_reorder(const void* src, void* dst, const int32_t* parents, const int32_t* lengths, int64_t L,
                                int32_t B, int32_t W, int32_t M, int32_t S, int32_t T, int64_t token, hipStream_t st) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst);
-  const uintptr_t all = at | static_cast<uintptr_t>(token);
-  if (at % 16 == 0 && T * token % 16 == 0) return move<u32x4>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
-  if (all % 4 == 0) return move<uint32_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
-  if (all % 2 == 0) return move<uint16_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
-  return move<uint8_t>(src, dst, parents, lengths, L, B, W, M, S, T, token, st);
+  const int64_t units = (T * token + kUnit - 1) / kUnit;
+  const int threads = units <= 64 ? 64 : kMoveThreads;  // of a run
+  const int64_t chunks = (units + threads - 1) / threads;
+  const int64_t items = L * B * S * chunks;
+  const bool in_place = src == dst;
+  const char* s = static_cast<const char*>(src);
+  char* d = static_cast<char*>(dst);
+#define DSPARK_MOVE(MB)                                                                                        \
+  DSPARK_LAUNCH("beam_reorder", (beam_reorder_kernel<MB>), grid, dim3(threads), 0, st, s, d, parents, \
+                lengths, base, chunks, B, W, M, S, T, token, in_place ? 0 : kNotInPlace)
+  for (int64_t base = 0; base < items; base += kMaxGrid) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items - base, kMaxGrid)));
+    if (M <= 4)
+      DSPARK_MOVE(4);
+    else if (M <= 8 || !in_place)
+      DSPARK_MOVE(8);
+    else if (M <= 16)
+      DSPARK_MOVE(16);
+    else
+      DSPARK_MOVE(32);
+  }
+#undef DSPARK_MOVE
+  return hipGetLastError();
 }
 
 }  // namespace dspark

@@ -552,6 +552,23 @@ def test_beam_reorder_at_odd_addresses():
         assert torch.equal(ds.dspark_beam_reorder(src, p, out=dst), want)
 
 
+@pytest.mark.parametrize("T", [13, 47, 48, 1100])
+def test_beam_reorder_every_last_byte(T):
+    """Lengths in bytes from none on, to new states and in place."""
+    B, W = 40, 5
+    rng = np.random.default_rng(T)
+    state = torch.from_numpy(rng.integers(0, 256, (2, B, W, T)).astype(np.uint8)).to(G.DEV)
+    parents = rng.integers(0, W, (B, W)).astype(np.int32)
+    lengths = np.minimum(np.arange(B) + (T - B if T > 100 else 0), T).astype(np.int32)
+    args = dict(batch_dim=1, lengths=torch.from_numpy(lengths).to(G.DEV), length_dim=3)
+    p = torch.from_numpy(parents).to(G.DEV)
+    fill = torch.full_like(state, 77)
+    want = ref.reorder(state.cpu().numpy(), parents, 1, lengths, 3, fill.cpu().numpy())
+    assert np.array_equal(ds.dspark_beam_reorder(state, p, out=fill, **args).cpu().numpy(), want)
+    want = ref.reorder(state.cpu().numpy(), parents, 1, lengths, 3, state.cpu().numpy())
+    assert np.array_equal(ds.dspark_beam_reorder(state, p, out=state, **args).cpu().numpy(), want)
+
+
 def test_beam_reorder_past_32_bit_offsets():
     T = 36_000_000  # a beam of 2.3 GB
     state = torch.zeros((1, 2, T, 64), dtype=torch.uint8, device=G.DEV)
