@@ -732,9 +732,10 @@ __global__ __launch_bounds__(kMergeThreads) void top_merge_kernel(const uint64_t
 //    of 256 threads), of up to 4 for larger K, whose bound comes from the groups'
 //    (20000 rows of 8000, K = 100: 193 against 226; 5000 of 20000, K = 64: 87
 //    against 75);
-//  * 512 threads for few long rows: 256 rows of 129280 bf16 17.7 us against 21.3 of 256
-//    threads; 700 rows 49 against 43 (several workgroups of 256 share a compute unit,
-//    and one's tail runs beside the others' streams);
+//  * 512 threads for long rows that have a compute unit each: 256 rows of 129280 bf16
+//    17.7 us against 21.3 of 256 threads, 128 rows of 50257 11.8 against 13.7; 300 rows
+//    of 90000 20.2 against 18.5, 700 of 129280 49 against 43 (several workgroups of
+//    256 share a compute unit, and one's tail runs beside the others' streams);
 //  * several segments a row only where one cannot hold it: the merge is a launch
 //    more (64 rows of 129280: 17 us against 16 with one; one row: 13 against 15, less
 //    than the second launch costs the host).
@@ -751,7 +752,7 @@ TopSplit top_split(int epl, int64_t R, int32_t V, int32_t K, bool any) {
   if (R >= 2048 && q <= (K <= 32 ? TopCaps<64>::kG : 4) * 64 * kL) {
     s.NT = 64;
     most = TopCaps<64>::kG;
-  } else if (q > 4 * 256 * kL && R <= 512) {
+  } else if (q > 4 * 256 * kL && R <= 256) {
     s.NT = 512;
     most = TopCaps<512>::kG;
   } else {
